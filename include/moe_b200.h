@@ -458,6 +458,105 @@ int moe_forward(const moe_shape* shape, const void* x, const float* router_w, fl
                 float* x_perm_scales, void* y_perm, void* y_shared, void* y, void* ws,
                 void* stream);
 
+/* ---- products by expert and layer norm, outside the fused expert FFN -----------
+ * These calls take their sizes directly (no moe_shape).  Conventions as above:
+ * device pointers, row-major, 16-byte aligned, nothing allocated, work only
+ * enqueued on `stream`.
+ *
+ * Ragged rows: expert e owns rows offsets[e] .. offsets[e+1]-1 (int32
+ * [experts+1], on the device, as moe_dispatch writes them; offsets NULL means
+ * one expert that owns all rows).  An expert may own no rows.  Rows before
+ * offsets[0] and from offsets[experts] on belong to nobody: they are neither
+ * used nor written.  An expert whose offsets do not satisfy
+ * 0 <= offsets[e] <= offsets[e+1] <= rows counts as empty and sets
+ * MOE_DEV_BAD_INDEX; ranges must not overlap.
+ *
+ * `ws`: moe_matmul_workspace_size() bytes, 256-byte aligned, zeroed once
+ * (moe_workspace_init); it holds the status word, so any workspace of this
+ * library serves, and calls on several streams or captured graphs may share
+ * it.  After MOE_DEV_WAIT_TIMEOUT clear it before the next call.
+ *
+ * Supported: experts <= 384; for BF16 n and k multiples of 8; for FP8 k (and
+ * for the input gradient n) a multiple of 16; else MOE_ERR_UNSUPPORTED.  A
+ * non-positive size, a negative row count, a NULL or misaligned pointer gives
+ * MOE_ERR_ARG.  rows = 0 is allowed (x, dy, y, dx may then be NULL). */
+size_t moe_matmul_workspace_size(void);
+
+/* Grouped matmul: y[r] = x[r] W_e^T for the rows r of each expert e.
+ *   x [rows, k], w [experts, n, k], y [rows, n]; dtype MOE_DTYPE_BF16 (tensor
+ *   cores, fp32 accumulation, one rounding) or MOE_DTYPE_FP32.
+ * moe_grouped_matmul_dx: dx[r] = dy[r] W_e, dy [rows, n], dx [rows, k].
+ * moe_grouped_matmul_dw: dw_e = sum over e's rows of dy[r]^T x[r], dw
+ *   [experts, n, k], written whole: an expert without rows gets zeros.  Rows
+ *   that belong to nobody do not reach it, whatever they hold. */
+int moe_grouped_matmul(const void* x, int64_t rows, const int32_t* offsets, int experts,
+                       const void* w, int n, int k, int dtype, void* y, void* ws, void* stream);
+int moe_grouped_matmul_dx(const void* dy, int64_t rows, const int32_t* offsets, int experts,
+                          const void* w, int n, int k, int dtype, void* dx, void* ws,
+                          void* stream);
+int moe_grouped_matmul_dw(const void* dy, const void* x, int64_t rows, const int32_t* offsets,
+                          int experts, int n, int k, int dtype, void* dw, void* ws, void* stream);
+
+/* 8-bit formats of the row codes. */
+enum {
+  MOE_FP8_E4M3 = 0,
+  MOE_FP8_E5M2 = 1
+};
+
+/* FP8 quantisation ([P1] 4.1: online max-abs scales).  top = 448 (E4M3) or
+ * 57344 (E5M2); scale = amax / top and inverse = top * (1 / amax), each
+ * operation rounded to fp32; code = round-to-nearest-even with saturation of
+ * v * inverse; all zeros: scale 1; amax below 2^-100 counts as 2^-100.
+ * (moe_dispatch and moe_quantize_weights round top / amax once: a value within
+ * an fp32 step of the middle between two codes may take the other one there.)
+ * moe_quantize_rows_fp8: per 1x128 tile of each row (the last tile may be
+ *   narrower), x [rows, cols] bf16, codes [rows, cols], scales block-major
+ *   [ceil(cols/128), scale_ld] fp32, scale_ld >= rows (columns past `rows` are
+ *   not written), cols % 16 == 0.
+ * moe_quantize_blocks_fp8: E4M3 per 128x128 block (edge blocks may be
+ *   smaller), w [experts, n, k] bf16, codes [experts, n, k], scales
+ *   [experts, ceil(n/128), ceil(k/128)] fp32, k % 16 == 0. */
+int moe_quantize_rows_fp8(const void* x, int64_t rows, int cols, int format, uint8_t* codes,
+                          float* scales, int64_t scale_ld, void* stream);
+int moe_quantize_blocks_fp8(const void* w, int experts, int n, int k, uint8_t* codes,
+                            float* scales, void* stream);
+
+/* Block-scaled FP8 matmul, dense (offsets NULL) or by expert:
+ *   y[r, j]  = sum_b x_scales[b, r] w_scales[e, j/128, b] sum_{i in block b} x[r, i] w[e, j, i]
+ * with x_codes [rows, k] in x_format, w_codes [experts, n, k] E4M3 and the
+ * scales laid out as the quantisers (and moe_dispatch, for x) write them; each
+ * 128-wide block is summed on the tensor cores and added in fp32; y [rows, n]
+ * bf16, one rounding.
+ * moe_matmul_fp8_dx: the input gradient from the same weight codes and scales,
+ *   dx[r, i] = sum_b dy_scales[b, r] w_scales[e, b, i/128] sum_{j in block b} dy[r, j] w[e, j, i]
+ * with dy_codes [rows, n] quantised along n; dx [rows, k] bf16. */
+int moe_matmul_fp8(const void* x_codes, int x_format, const float* x_scales, int64_t scale_ld,
+                   int64_t rows, const int32_t* offsets, int experts, const void* w_codes,
+                   const float* w_scales, int n, int k, void* y, void* ws, void* stream);
+int moe_matmul_fp8_dx(const void* dy_codes, int dy_format, const float* dy_scales,
+                      int64_t scale_ld, int64_t rows, const int32_t* offsets, int experts,
+                      const void* w_codes, const float* w_scales, int n, int k, void* dx, void* ws,
+                      void* stream);
+
+/* Layer norm of the rows in front of the layer, 1 <= d <= 16384:
+ *   mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = (x - mean) rstd weight + bias
+ *   x, y [rows, d] bf16 or fp32 (dtype); weight [d], bias [d] (or NULL) fp32;
+ *   mean, rstd [rows] fp32 out, for the backward.
+ * moe_layer_norm_backward: with h = dy weight and z = (x - mean) rstd,
+ *   dx = rstd (h - mean(h) - z mean(h z))       [rows, d], one rounding
+ *   dweight = sum over rows of dy z, dbias = sum over rows of dy   [d] fp32
+ *   dbias may be NULL.  ws: moe_layer_norm_workspace_size(rows, d) bytes of
+ *   scratch, 256-byte aligned; calls that may run at the same time (streams,
+ *   graphs) need one each.  The column sums run in a fixed order.
+ * Statistics and sums are fp32. */
+size_t moe_layer_norm_workspace_size(int64_t rows, int d);
+int moe_layer_norm(const void* x, const float* weight, const float* bias, float eps, int64_t rows,
+                   int d, int dtype, void* y, float* mean, float* rstd, void* stream);
+int moe_layer_norm_backward(const void* dy, const void* x, const float* weight, const float* mean,
+                            const float* rstd, int64_t rows, int d, int dtype, void* dx,
+                            float* dweight, float* dbias, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

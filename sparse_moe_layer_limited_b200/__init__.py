@@ -12,6 +12,9 @@ from ._lib import (  # noqa: F401
     DTYPE_BF16, DTYPE_E4M3, DTYPE_FP32, MoEError, MoEShape, check_shape, lib, moe_bias_update,
     moe_combine, moe_dispatch, moe_dispatch_noalloc, moe_expert_ffn, moe_expert_ffn_gathered,
     moe_gather_rows, moe_expert_ffn_combine,
+    layer_norm_workspace_size, matmul_workspace_size, moe_grouped_matmul, moe_grouped_matmul_dx,
+    moe_grouped_matmul_dw, moe_layer_norm, moe_layer_norm_backward, moe_matmul_fp8,
+    moe_matmul_fp8_dx, moe_quantize_blocks_fp8, moe_quantize_rows_fp8,
     moe_forward, moe_pack_w13, moe_quantize_weights,
     moe_read_device_status, moe_read_gemm_clock, moe_route, moe_route_softmax, moe_workspace_init, shape,
     status_string,

@@ -18,6 +18,8 @@ DTYPE_FP32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4, -5
 
 _c_p = ctypes.c_void_p
+_c_i = ctypes.c_int
+_c_i64 = ctypes.c_int64
 
 
 class MoEShape(ctypes.Structure):
@@ -73,6 +75,23 @@ _SIGS = {
                                        _c_p, _c_p]),
     "moe_pack_w13": (ctypes.c_int, [ctypes.POINTER(MoEShape)] + [_c_p] * 4),
     "moe_quantize_weights": (ctypes.c_int, [ctypes.POINTER(MoEShape)] + [_c_p] * 7),
+    "moe_matmul_workspace_size": (ctypes.c_size_t, []),
+    "moe_grouped_matmul": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i, _c_p, _c_i, _c_i, _c_i]
+                           + [_c_p] * 3),
+    "moe_grouped_matmul_dx": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i, _c_p, _c_i, _c_i, _c_i]
+                              + [_c_p] * 3),
+    "moe_grouped_matmul_dw": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_i, _c_i, _c_i, _c_i]
+                              + [_c_p] * 3),
+    "moe_quantize_rows_fp8": (ctypes.c_int, [_c_p, _c_i64, _c_i, _c_i, _c_p, _c_p, _c_i64, _c_p]),
+    "moe_quantize_blocks_fp8": (ctypes.c_int, [_c_p, _c_i, _c_i, _c_i] + [_c_p] * 3),
+    "moe_matmul_fp8": (ctypes.c_int, [_c_p, _c_i, _c_p, _c_i64, _c_i64, _c_p, _c_i, _c_p, _c_p,
+                                      _c_i, _c_i] + [_c_p] * 3),
+    "moe_matmul_fp8_dx": (ctypes.c_int, [_c_p, _c_i, _c_p, _c_i64, _c_i64, _c_p, _c_i, _c_p, _c_p,
+                                         _c_i, _c_i] + [_c_p] * 3),
+    "moe_layer_norm_workspace_size": (ctypes.c_size_t, [_c_i64, _c_i]),
+    "moe_layer_norm": (ctypes.c_int, [_c_p, _c_p, _c_p, ctypes.c_float, _c_i64, _c_i, _c_i]
+                       + [_c_p] * 4),
+    "moe_layer_norm_backward": (ctypes.c_int, [_c_p] * 5 + [_c_i64, _c_i, _c_i] + [_c_p] * 5),
     "moe_forward": (ctypes.c_int, [ctypes.POINTER(MoEShape), _c_p, _c_p, _c_p, ctypes.c_float]
                     + [_c_p] * 17),
 }
@@ -387,3 +406,194 @@ def moe_forward(s, x, router_w, bias, gamma, w13, w2, w13_scales, w2_scales, top
           _ptr(topk_idx), _ptr(topk_gate), _ptr(counts), _ptr(offsets), _ptr(perm_tok),
           _ptr(slot), _ptr(x_perm), _ptr(x_perm_scales), _ptr(y_perm), _ptr(y_shared), _ptr(y),
           _ptr(ws), _stream(stream))
+
+
+# ---- products by expert and layer norm ------------------------------------------------
+# These calls read their sizes from the tensors and launch on the tensors' own
+# device, whichever device is current; all tensors of a call must share it.
+
+_DTYPES = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16}
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _tensor(t, name, dtype, shape, like):
+    """The data pointer of a contiguous CUDA tensor of this dtype and shape on
+    the device of `like`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on {like.device}")
+    return _ptr(t)
+
+
+def _scratch(t, name, size, like):
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on {like.device}")
+    if t.numel() * t.element_size() < size:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, needs {size}")
+    return _ptr(t)
+
+
+def _matrix(t, name, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got {t.dim()}")
+    return tuple(t.shape)
+
+
+def _offsets(offsets, experts, like):
+    if offsets is None:
+        if experts != 1:
+            raise ValueError("offsets: required for more than one expert")
+        return None
+    return _tensor(offsets, "offsets", torch.int32, (experts + 1,), like)
+
+
+def _call_on(t, name, stream, *args):
+    """The C call on t's device: its current stream, or `stream`."""
+    dev = t.device
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, _stream(stream))
+
+
+def matmul_workspace_size() -> int:
+    return lib().moe_matmul_workspace_size()
+
+
+def layer_norm_workspace_size(rows, d) -> int:
+    return lib().moe_layer_norm_workspace_size(rows, d)
+
+
+def _mm_dtype(t, name):
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def moe_grouped_matmul(x, offsets, w, y, ws, stream=None):
+    """y[r] = x[r] @ w[e].T for the rows r of expert e: x [rows, k], w
+    [experts, n, k], y [rows, n], bf16 or fp32; offsets int32 [experts + 1] on
+    the device (None: one expert owns all rows); rows outside
+    offsets[0] .. offsets[-1] of y are left as they were."""
+    E, n, k = _matrix(w, "w", 3)
+    R = _matrix(x, "x", 2)[0]
+    dt = _mm_dtype(x, "x")
+    _call_on(x, "moe_grouped_matmul", stream, _tensor(x, "x", x.dtype, (R, k), x), R,
+             _offsets(offsets, E, x), E, _tensor(w, "w", x.dtype, (E, n, k), x), n, k, dt,
+             _tensor(y, "y", x.dtype, (R, n), x), _scratch(ws, "ws", 256, x))
+
+
+def moe_grouped_matmul_dx(dy, offsets, w, dx, ws, stream=None):
+    """dx[r] = dy[r] @ w[e]: the input gradient of moe_grouped_matmul (dy
+    [rows, n], dx [rows, k])."""
+    E, n, k = _matrix(w, "w", 3)
+    R = _matrix(dy, "dy", 2)[0]
+    dt = _mm_dtype(dy, "dy")
+    _call_on(dy, "moe_grouped_matmul_dx", stream, _tensor(dy, "dy", dy.dtype, (R, n), dy), R,
+             _offsets(offsets, E, dy), E, _tensor(w, "w", dy.dtype, (E, n, k), dy), n, k, dt,
+             _tensor(dx, "dx", dy.dtype, (R, k), dy), _scratch(ws, "ws", 256, dy))
+
+
+def moe_grouped_matmul_dw(dy, x, offsets, dw, ws, stream=None):
+    """dw[e] = dy[rows of e].T @ x[rows of e]: the weight gradient of
+    moe_grouped_matmul (dw [experts, n, k]; zeros for an expert without rows)."""
+    E, n, k = _matrix(dw, "dw", 3)
+    R = _matrix(dy, "dy", 2)[0]
+    dt = _mm_dtype(dy, "dy")
+    _call_on(dy, "moe_grouped_matmul_dw", stream, _tensor(dy, "dy", dy.dtype, (R, n), dy),
+             _tensor(x, "x", dy.dtype, (R, k), dy), R, _offsets(offsets, E, dy), E, n, k, dt,
+             _tensor(dw, "dw", dy.dtype, (E, n, k), dy), _scratch(ws, "ws", 256, dy))
+
+
+def _fp8_format(t, name):
+    if t.dtype not in _FP8:
+        raise TypeError(f"{name}: expected float8_e4m3fn or float8_e5m2, got {t.dtype}")
+    return _FP8[t.dtype]
+
+
+def _row_scales(scales, name, cols, like):
+    blocks, ld = _matrix(scales, name, 2)
+    return _tensor(scales, name, torch.float32, (-(-cols // 128), ld), like), ld
+
+
+def moe_quantize_rows_fp8(x, codes, scales, stream=None):
+    """x [rows, cols] bf16 -> codes [rows, cols] (float8_e4m3fn or float8_e5m2,
+    by the tensor's dtype) and scales [ceil(cols / 128), ld >= rows] fp32."""
+    R, C = _matrix(x, "x", 2)
+    fmt = _fp8_format(codes, "codes")
+    sp, ld = _row_scales(scales, "scales", C, x)
+    _call_on(x, "moe_quantize_rows_fp8", stream, _tensor(x, "x", torch.bfloat16, (R, C), x), R, C,
+             fmt, _tensor(codes, "codes", codes.dtype, (R, C), x), sp, ld)
+
+
+def moe_quantize_blocks_fp8(w, codes, scales, stream=None):
+    """w [experts, n, k] bf16 -> codes float8_e4m3fn [experts, n, k] and scales
+    fp32 [experts, ceil(n / 128), ceil(k / 128)], one per 128x128 block."""
+    E, n, k = _matrix(w, "w", 3)
+    _call_on(w, "moe_quantize_blocks_fp8", stream,
+             _tensor(w, "w", torch.bfloat16, (E, n, k), w), E, n, k,
+             _tensor(codes, "codes", torch.float8_e4m3fn, (E, n, k), w),
+             _tensor(scales, "scales", torch.float32, (E, -(-n // 128), -(-k // 128)), w))
+
+
+def _matmul_fp8(name, rows, scales, offsets, w, w_scales, out, ws, stream, dx):
+    E, n, k = _matrix(w, "w", 3)
+    R = _matrix(rows, "codes", 2)[0]
+    fmt = _fp8_format(rows, "codes")
+    cin, cout = (n, k) if dx else (k, n)
+    sp, ld = _row_scales(scales, "scales", cin, rows)
+    _call_on(rows, name, stream, _tensor(rows, "codes", rows.dtype, (R, cin), rows), fmt, sp, ld,
+             R, _offsets(offsets, E, rows), E,
+             _tensor(w, "w", torch.float8_e4m3fn, (E, n, k), rows),
+             _tensor(w_scales, "w_scales", torch.float32, (E, -(-n // 128), -(-k // 128)), rows),
+             n, k, _tensor(out, "out", torch.bfloat16, (R, cout), rows),
+             _scratch(ws, "ws", 256, rows))
+
+
+def moe_matmul_fp8(x, x_scales, offsets, w, w_scales, y, ws, stream=None):
+    """y[r] = dequantised x[r] @ dequantised w[e].T: x codes [rows, k] with
+    scales [ceil(k / 128), ld >= rows], w codes float8_e4m3fn [experts, n, k]
+    with scales [experts, ceil(n / 128), ceil(k / 128)], y [rows, n] bf16;
+    offsets as at moe_grouped_matmul."""
+    _matmul_fp8("moe_matmul_fp8", x, x_scales, offsets, w, w_scales, y, ws, stream, False)
+
+
+def moe_matmul_fp8_dx(dy, dy_scales, offsets, w, w_scales, dx, ws, stream=None):
+    """dx[r] = dequantised dy[r] @ dequantised w[e], from the forward's weight
+    codes: dy codes [rows, n] with scales [ceil(n / 128), ld >= rows], dx
+    [rows, k] bf16."""
+    _matmul_fp8("moe_matmul_fp8_dx", dy, dy_scales, offsets, w, w_scales, dx, ws, stream, True)
+
+
+def moe_layer_norm(x, weight, bias, eps, y, mean, rstd, stream=None):
+    """y = (x - mean) * rstd * weight + bias over the last dimension of x
+    [rows, d] (bf16 or fp32; weight, bias fp32 [d], bias may be None); writes
+    the rows' mean and rstd (fp32 [rows]) for the backward."""
+    R, d = _matrix(x, "x", 2)
+    dt = _mm_dtype(x, "x")
+    f32 = torch.float32
+    _call_on(x, "moe_layer_norm", stream, _tensor(x, "x", x.dtype, (R, d), x),
+             _tensor(weight, "weight", f32, (d,), x),
+             None if bias is None else _tensor(bias, "bias", f32, (d,), x), eps, R, d, dt,
+             _tensor(y, "y", x.dtype, (R, d), x), _tensor(mean, "mean", f32, (R,), x),
+             _tensor(rstd, "rstd", f32, (R,), x))
+
+
+def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None):
+    """Gradients of moe_layer_norm: dx [rows, d] in x's type, dweight and dbias
+    fp32 [d] (dbias may be None).  ws: layer_norm_workspace_size(rows, d) bytes."""
+    R, d = _matrix(x, "x", 2)
+    dt = _mm_dtype(x, "x")
+    f32 = torch.float32
+    _call_on(x, "moe_layer_norm_backward", stream, _tensor(dy, "dy", x.dtype, (R, d), x),
+             _tensor(x, "x", x.dtype, (R, d), x), _tensor(weight, "weight", f32, (d,), x),
+             _tensor(mean, "mean", f32, (R,), x), _tensor(rstd, "rstd", f32, (R,), x), R, d, dt,
+             _tensor(dx, "dx", x.dtype, (R, d), x), _tensor(dweight, "dweight", f32, (d,), x),
+             None if dbias is None else _tensor(dbias, "dbias", f32, (d,), x),
+             _scratch(ws, "ws", layer_norm_workspace_size(R, d), x))

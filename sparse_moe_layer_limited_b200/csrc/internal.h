@@ -199,4 +199,33 @@ cudaError_t launch_quantize_weights(const moe_shape& s, const void* w13, const v
                                     void* w13_q, float* w13_scales, void* w2_q,
                                     float* w2_scales, cudaStream_t st);
 
+// ---- operators around the fused expert FFN ---------------------------------------
+// Grouped matmul (grouped_matmul.cu, grouped_matmul_fp32.cu).  mode 0: x [R, k]
+// -> y [R, n]; mode 1: dy [R, n] -> dx [R, k]; the fp32 launcher's mode 2:
+// a = dy, b = x -> dw [E, n, k].  offsets NULL: one group of all rows.
+int launch_grouped_matmul_bf16(int mode, const void* rows, int R, const int32_t* offsets, int E,
+                               const void* w, int n, int k, void* out, void* ws, cudaStream_t st);
+int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const int32_t* offsets,
+                                  int E, int n, int k, void* dw, void* ws, cudaStream_t st);
+int launch_grouped_matmul_fp32(int mode, const float* a, const float* b, int R,
+                               const int32_t* offsets, int E, int n, int k, float* out, void* ws,
+                               cudaStream_t st);
+// Block-scaled FP8 matmul and its quantisers (matmul_fp8.cu).
+int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scales,
+                      long long sa_ld, int R, const int32_t* offsets, int E, const void* w,
+                      const float* w_scales, int n, int k, void* out, void* ws, cudaStream_t st);
+cudaError_t launch_quantize_rows_fp8(const void* x, long long rows, int cols, int e5m2,
+                                     uint8_t* codes, float* scales, long long sc_ld,
+                                     cudaStream_t st);
+cudaError_t launch_quantize_blocks_fp8(const void* w, int E, int n, int k, uint8_t* codes,
+                                       float* scales, cudaStream_t st);
+// Layer norm (layer_norm.cu); the backward's ws holds layer_norm_ws_bytes.
+int layer_norm_max_d();
+size_t layer_norm_ws_bytes(int R, int d);
+cudaError_t launch_layer_norm(int dtype, const void* x, const float* w, const float* b, float eps,
+                              int R, int d, void* y, float* mean, float* rstd, cudaStream_t st);
+cudaError_t launch_layer_norm_backward(int dtype, const void* dy, const void* x, const float* w,
+                                       const float* mean, const float* rstd, int R, int d,
+                                       void* dx, float* dw, float* db, void* ws, cudaStream_t st);
+
 }  // namespace moe

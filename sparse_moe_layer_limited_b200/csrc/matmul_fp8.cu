@@ -1,0 +1,517 @@
+// Block-scaled FP8 matmul, dense or by expert over ragged rows:
+//   forward         y[r, j]  = sum_b sa[r, b] sw[e, j/128, b] sum_{i in b} qa[r, i] qw[e, j, i]
+//   input gradient  dx[r, i] = sum_b sa[r, b] sw[e, b, i/128] sum_{j in b} qa[r, j] qw[e, j, i]
+// b runs over the 128-wide blocks of the contraction index.  Rows carry one
+// fp32 scale per 1x128 tile (E4M3 or E5M2 codes), the weight one per 128x128
+// block (E4M3).  The input gradient reads the same codes and scales as the
+// forward: its weight operand has the contraction index outermost.
+//
+// Each 128-wide slice of a 128 x 256 output tile is one product on the tensor
+// cores (fp32, exact per-slice sums of the codes' products up to fp32
+// accumulation) into one of two 256-column TMEM buffers; eight epilogue warps
+// multiply it by the two scales and add it to fp32 registers, 128 running sums
+// a thread, while the next slice fills the other buffer.  The scales are read
+// from global memory four slices ahead.  The result is rounded once to bf16.
+//
+// Also here: the quantisers that make the codes, per 1x128 tile of a row and
+// per 128x128 block (tile_scale below).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "epilogue.cuh"
+#include "fp8_util.cuh"
+#include "internal.h"
+#include "matmul_util.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int PBM = 128, PBN = 256, PBK = 128;
+constexpr int PStages = 4;
+constexpr int PABytes = PBM * PBK;
+constexpr int PStageBytes = PABytes + PBN * PBK;
+constexpr int PEpiWarps = 8;
+constexpr int PThreads = 64 + 32 * PEpiWarps;
+constexpr int PStg = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
+constexpr int PCols = PBN / 2;  // columns per epilogue warp
+constexpr int kAhead = 4;       // slices whose scales are loaded together
+
+constexpr size_t fp8_mm_smem(int E) {
+  return 1024 + (size_t)PStages * PStageBytes + PEpiWarps * PStg + 256 + (size_t)(E + 1) * 4;
+}
+static_assert(fp8_mm_smem(kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
+
+struct alignas(64) PArgs {
+  CUtensorMap tmA;    // row codes [R, K], box {128, 128}
+  CUtensorMap tmA32;  // the same, box {128, 32}
+  CUtensorMap tmB;    // weight codes [E, n, k]: fwd box {128, 64, 1}, dx box {128, 128, 1}
+  CUtensorMap tmOut;  // out [R, cols] bf16, box {64, 32} (cols % 8 == 0)
+  const int32_t* offsets;
+  const float* sa;  // [KB, sa_ld]
+  const float* sw;  // [E, ceil(n/128), ceil(k/128)]
+  __nv_bfloat16* out;
+  uint32_t* status;
+  long long sa_ld;
+  int E, R;
+  int cols, kdim;
+  int nb, kb;     // blocks along n and k
+  uint32_t a_fmt;
+};
+
+__device__ __forceinline__ void fma2(float& a0, float& a1, float x0, float x1, float s) {
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
+      "mov.b64 rc, {%0, %1};\n\tfma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1), "f"(s));
+}
+
+template <bool kDx>
+__global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
+    const __grid_constant__ PArgs args) {
+  constexpr int kChunkCols = kDx ? 128 : 64;           // weight columns per TMA box
+  constexpr int kChunk = kChunkCols * PBK;             // its bytes
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = base + (size_t)PStages * PStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + PEpiWarps * PStg);
+  uint64_t* full = bars;
+  uint64_t* empty = full + PStages;
+  uint64_t* sfull = empty + PStages;  // [2] slice buffer written
+  uint64_t* sempty = sfull + 2;       // [2] slice buffer read
+  uint64_t* drain = sempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int NT = (args.cols + PBN - 1) / PBN;
+  const int KB = (args.kdim + PBK - 1) / PBK;
+
+  if (tid == 0) {
+    for (int s = 0; s < PStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sfull[a], 1);
+      mbar_init(&sempty[a], PEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0) ragged_schedule(args.offsets, args.E, args.R, PBM, NT, start, args.status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int total = start[args.E];
+
+  struct Unit {
+    int g, first, rows, m, n;
+  };
+  auto decode = [&](int u) {
+    Unit t;
+    bool bad = false;
+    t.g = ragged_group(start, args.E, u);
+    t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
+    const int mt = (t.rows + PBM - 1) / PBM;
+    const int local = u - start[t.g];
+    t.n = local / mt;
+    t.m = local - t.n * mt;
+    return t;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&args.tmA);
+      tma_prefetch_desc(&args.tmB);
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Unit t = decode(u);
+        const int nc =
+            min(PBN / kChunkCols, (args.cols - t.n * PBN + kChunkCols - 1) / kChunkCols);
+        const int na = min(4, (t.rows - t.m * PBM + 31) / 32);
+        const int r = t.first + t.m * PBM;
+        const uint32_t bytes = (uint32_t)(nc * kChunk + na * 32 * PBK);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mm_wait(&empty[stage], phase ^ 1u, args.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = base + (size_t)stage * PStageBytes;
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          if (na == 4) {
+            tma_load_2d(sa, &args.tmA, kb * PBK, r, &full[stage]);
+          } else {
+            for (int c = 0; c < na; ++c)
+              tma_load_2d(sa + c * (32 * PBK), &args.tmA32, kb * PBK, r + 32 * c, &full[stage]);
+          }
+          for (int c = 0; c < nc; ++c) {
+            const int col = t.n * PBN + kChunkCols * c;
+            if constexpr (kDx)
+              tma_load_3d(sa + PABytes + c * kChunk, &args.tmB, col, kb * PBK, t.g, &full[stage]);
+            else
+              tma_load_3d(sa + PABytes + c * kChunk, &args.tmB, kb * PBK, col, t.g, &full[stage]);
+          }
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == PStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        for (int s = 0; s < PStages; ++s)
+          if ((issued >> s) & 1u)
+            mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, slice = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Unit t = decode(u);
+        const int width = min(PBN, args.cols - t.n * PBN);
+        const uint32_t idesc = idesc_f8_f32(PBM, (width + 15) / 16 * 16, args.a_fmt, kF8E4M3) |
+                               (kDx ? kIdescBMn : 0u);
+        for (int kb = 0; kb < KB; ++kb, ++slice) {
+          const uint32_t sb = slice & 1u;
+          if (!mm_wait(&sempty[sb], ((slice >> 1) & 1u) ^ 1u, args.status) ||
+              !mm_wait(&full[stage], phase, args.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(base + (size_t)stage * PStageBytes), b0 = a0 + PABytes;
+#pragma unroll
+          for (int k = 0; k < PBK / 32; ++k)
+            mma_e4m3(tmem_base + sb * PBN, smem_desc_sw128(a0 + k * 32),
+                     kDx ? smem_desc_mn_sw128(b0 + k * 4096, kChunk) : smem_desc_sw128(b0 + k * 32),
+                     idesc, k != 0);
+          mma_commit(&empty[stage]);
+          mma_commit(&sfull[sb]);
+          if (++stage == PStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      mma_commit(drain);
+      mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
+    }
+  } else {
+    // ---- promotion and epilogue: two warps per lane quadrant, 128 columns each ----
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stg = staging + (size_t)(warp - 2) * PStg;
+    const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + half * PCols;
+    const bool tma_out = (args.cols & 7) == 0;
+    uint32_t slice = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      const Unit t = decode(u);
+      const int r0 = t.m * PBM + q * 32, left = t.rows - r0;
+      const int col0 = t.n * PBN + half * PCols;
+      const bool live = left > 0 && col0 < args.cols;  // warp-uniform
+      // scales: sa[kb][row], and the weight block of this warp's columns
+      const int row = min(t.first + r0 + lane, args.R - 1);
+      const float* sa = args.sa + row;
+      const float* sw = args.sw + (size_t)t.g * args.nb * args.kb +
+                        (kDx ? (size_t)(col0 / 128) : (size_t)(col0 / 128) * args.kb);
+      const int sw_step = kDx ? args.kb : 1;
+      float acc[PCols];
+#pragma unroll
+      for (int i = 0; i < PCols; ++i) acc[i] = 0.f;
+      float cur[kAhead], nxt[kAhead];
+      auto scales = [&](float (&s)[kAhead], int kb) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          s[j] = 0.f;
+          if (live && kb + j < KB)
+            s[j] = __ldg(sa + (size_t)(kb + j) * args.sa_ld) *
+                   __ldg(sw + (size_t)(kb + j) * sw_step);
+        }
+      };
+      scales(nxt, 0);
+      for (int kb = 0; kb < KB && ok; kb += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) cur[j] = nxt[j];
+        scales(nxt, kb + kAhead);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (kb + j >= KB) break;
+          const uint32_t sb = slice & 1u;
+          if (!mm_wait(&sfull[sb], (slice >> 1) & 1u, args.status)) {
+            ok = false;
+            break;
+          }
+          ++slice;
+          tc_fence_after();
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < PCols; c += 32) {
+              uint32_t p0[16], p1[16];
+              tmem_ld16(tbase + sb * PBN + c, p0);
+              tmem_ld16(tbase + sb * PBN + c + 16, p1);
+              tmem_wait_ld();
+              if (c + 32 == PCols) {  // the slice is in registers: hand the buffer back
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[sb]);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                fma2(acc[c + i], acc[c + i + 1], __uint_as_float(p0[i]),
+                     __uint_as_float(p0[i + 1]), cur[j]);
+                fma2(acc[c + 16 + i], acc[c + 17 + i], __uint_as_float(p1[i]),
+                     __uint_as_float(p1[i + 1]), cur[j]);
+              }
+            }
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[sb]);
+          }
+        }
+      }
+      if (!ok) break;
+      if (!live) continue;
+#pragma unroll
+      for (int c = 0; c < PCols; c += 64) {
+        const int col = col0 + c;
+        if (col >= args.cols) break;
+        const bool by_tma = tma_out && left >= 32;
+        if (lane == 0) bulk_wait_read_all();  // the previous piece has left the buffer
+        __syncwarp();
+        uint8_t* my = stg + lane * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float* a = acc + c + 8 * j;
+          const uint4 v = make_uint4(bf16x2_bits(a[0], a[1]), bf16x2_bits(a[2], a[3]),
+                                     bf16x2_bits(a[4], a[5]), bf16x2_bits(a[6], a[7]));
+          *reinterpret_cast<uint4*>(my + ((j ^ (lane & 7)) << 4)) = v;
+        }
+        if (by_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&args.tmOut, stg, col, t.first + r0);
+            bulk_commit_group();
+          }
+        } else {
+          // ragged last rows, or rows that do not start on 16 bytes: the warp
+          // writes one row's 64 columns at a time
+          __syncwarp();
+          const int rows = min(32, left), wide = min(64, args.cols - col);
+          for (int i = 0; i < rows; ++i) {
+            __nv_bfloat16* dst =
+                args.out + (size_t)(t.first + r0 + i) * (size_t)args.cols + col;
+            for (int e = lane; e < wide; e += 32) {
+              const int piece = (e >> 3) ^ (i & 7);
+              dst[e] = *reinterpret_cast<const __nv_bfloat16*>(stg + i * 128 + piece * 16 +
+                                                               (e & 7) * 2);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ---- quantisers -------------------------------------------------------------------
+// top: the largest finite code (448 E4M3, 57344 E5M2).  scale = amax / top and
+// inverse = top * (1 / amax), each operation rounded to fp32; all zeros give
+// scale 1.  A max-abs below 2^-100 counts as 2^-100: its inverse would pass
+// the fp32 range and turn the tile's zeros into NaN.
+struct TileScale {
+  float scale, inverse;
+};
+__device__ __forceinline__ TileScale tile_scale(float amax, float top) {
+  if (amax == 0.f) return {1.f, 0.f};
+  amax = fmaxf(amax, 0x1p-100f);
+  return {__fdiv_rn(amax, top), __fmul_rn(top, __frcp_rn(amax))};
+}
+// 8 values -> 8 codes: round to nearest even with saturation; NaN stays NaN.
+template <bool kE5M2>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inverse) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fmul_rn(v[2 * p], inverse), __fmul_rn(v[2 * p + 1], inverse)),
+        __NV_SATFINITE, kE5M2 ? __NV_E5M2 : __NV_E4M3);
+    w[p >> 1] |= (uint32_t)c2 << (16 * (p & 1));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Rows [rows, cols], cols a multiple of 16: one half-warp per 1x128 tile, 8
+// values per lane; lanes past the last column hold zeros.
+template <bool kE5M2>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16* __restrict__ x,
+                                                            long long rows, int cols,
+                                                            uint8_t* __restrict__ q,
+                                                            float* __restrict__ sc,
+                                                            long long sc_ld) {
+  const int tiles_per_row = (cols + QB - 1) / QB;
+  const long long tiles = rows * tiles_per_row;
+  const int l16 = threadIdx.x & 15;
+  const long long hw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
+  const long long stride = ((long long)gridDim.x * blockDim.x) >> 4;
+  // every half-warp walks the same number of tiles: the shuffles stay converged
+  const long long iters = (tiles + stride - 1) / stride;
+  for (long long it = 0; it < iters; ++it) {
+    const long long tile = hw + it * stride;
+    const bool live = tile < tiles;
+    const long long r = live ? tile / tiles_per_row : 0;
+    const int b = live ? (int)(tile - r * tiles_per_row) : 0;
+    const int c = b * QB + 8 * l16;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const bool inside = live && c < cols;
+    if (inside) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(x + r * cols + c)), v);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const TileScale s = tile_scale(amax, kE5M2 ? 57344.f : 448.f);
+    if (inside) *reinterpret_cast<uint2*>(q + r * cols + c) = codes8<kE5M2>(v, s.inverse);
+    if (live && l16 == 0) sc[(long long)b * sc_ld + r] = s.scale;
+  }
+}
+
+// One 128x128 block of one matrix per CTA of 128 threads: sixteen lanes cover a
+// row's 128 columns with 16-byte loads, kept in registers for the second pass.
+__global__ void __launch_bounds__(128) quantize_blocks_kernel(const __nv_bfloat16* __restrict__ w,
+                                                              int n, int k, int nb, int kb,
+                                                              uint8_t* __restrict__ q,
+                                                              float* __restrict__ sc) {
+  __shared__ float red[4];
+  const long long blk = blockIdx.x;
+  const int bc = (int)(blk % kb);
+  const long long eb = blk / kb;
+  const int br = (int)(eb % nb);
+  const long long e = eb / nb;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int col = bc * QB + 8 * (lane & 15);
+  const int row0 = br * QB + warp * 32 + (lane >> 4);
+  const size_t at0 = ((size_t)e * n + row0) * (size_t)k + col;
+  uint4 raw[16];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row0 + 2 * i < n && col < k)
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(w + at0 + (size_t)(2 * i) * k));
+    float f[8];
+    bf16x8_to_f32(raw[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();
+  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const TileScale ts = tile_scale(amax, 448.f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (row0 + 2 * i >= n || col >= k) continue;
+    float f[8];
+    bf16x8_to_f32(raw[i], f);
+    *reinterpret_cast<uint2*>(q + at0 + (size_t)(2 * i) * k) = codes8<false>(f, ts.inverse);
+  }
+  if (t == 0) sc[blk] = ts.scale;
+}
+
+template <bool kDx>
+cudaError_t launch(const PArgs& a, cudaStream_t st) {
+  const size_t smem = fp8_mm_smem(a.E);
+  cudaError_t e = note_cuda(cudaFuncSetAttribute(matmul_fp8_kernel<kDx>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)smem),
+                            "fp8 matmul: set shared-memory size");
+  if (e != cudaSuccess) return e;
+  const long long mt = a.R / PBM + (a.R < a.E ? a.R : a.E);  // no more row tiles than this
+  const long long units = mt * ((a.cols + PBN - 1) / PBN);
+  const int grid = (int)(units < num_sms() ? units : num_sms());
+  matmul_fp8_kernel<kDx><<<grid, PThreads, smem, st>>>(a);
+  return note_cuda(cudaGetLastError(), "fp8 matmul launch");
+}
+
+}  // namespace
+
+// dx == 0: a [R, k], out [R, n]; dx == 1: a [R, n], out [R, k].  e5m2: a's format.
+int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scales, long long sa_ld,
+                      int R, const int32_t* offsets, int E, const void* w, const float* w_scales,
+                      int n, int k, void* out, void* ws, cudaStream_t st) {
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  PArgs a{};
+  a.offsets = offsets;
+  a.sa = a_scales;
+  a.sa_ld = sa_ld;
+  a.sw = w_scales;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.status = static_cast<uint32_t*>(ws);
+  a.E = E;
+  a.R = R;
+  a.cols = dx ? k : n;
+  a.kdim = dx ? n : k;
+  a.nb = (n + QB - 1) / QB;
+  a.kb = (k + QB - 1) / QB;
+  a.a_fmt = e5m2 ? kF8E5M2 : kF8E4M3;
+  const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E};
+  const uint64_t strides[2] = {(uint64_t)k, (uint64_t)k * n};
+  const uint32_t box[3] = {128, dx ? 128u : 64u, 1};
+  if (!make_map(&a.tmA, a_codes, U8, 1, a.kdim, R, PBK, 128) ||
+      !make_map(&a.tmA32, a_codes, U8, 1, a.kdim, R, PBK, 32) ||
+      !make_map_nd(&a.tmB, w, U8, 3, dims, strides, box) ||
+      (a.cols % 8 == 0 && !make_map_swizzled(&a.tmOut, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                             a.cols, R, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))) {
+    note_text("fp8 matmul: tensor-map encoding failed");
+    return MOE_ERR_CUDA;
+  }
+  const cudaError_t e = dx ? launch<true>(a, st) : launch<false>(a, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+cudaError_t launch_quantize_rows_fp8(const void* x, long long rows, int cols, int e5m2,
+                                     uint8_t* codes, float* scales, long long sc_ld,
+                                     cudaStream_t st) {
+  const long long tiles = rows * ((cols + QB - 1) / QB);
+  long long blocks = (tiles * 16 + 255) / 256;
+  if (blocks > 148 * 16) blocks = 148 * 16;
+  auto kernel = e5m2 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>;
+  kernel<<<(int)blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, codes,
+                                      scales, sc_ld);
+  return note_cuda(cudaGetLastError(), "row quantisation launch");
+}
+
+cudaError_t launch_quantize_blocks_fp8(const void* w, int E, int n, int k, uint8_t* codes,
+                                       float* scales, cudaStream_t st) {
+  const int nb = (n + QB - 1) / QB, kb = (k + QB - 1) / QB;
+  const long long blocks = (long long)E * nb * kb;
+  quantize_blocks_kernel<<<(unsigned)blocks, 128, 0, st>>>(static_cast<const __nv_bfloat16*>(w), n,
+                                                           k, nb, kb, codes, scales);
+  return note_cuda(cudaGetLastError(), "block quantisation launch");
+}
+
+}  // namespace moe

@@ -1,0 +1,125 @@
+// Shared by the grouped bf16 matmul (grouped_matmul.cu) and the block-scaled
+// FP8 matmul (matmul_fp8.cu): the ragged tile schedule, operand descriptors
+// for tiles whose contraction index is the outer one, and a bounded wait.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kMatmulMaxGroups = 384;  // tile table entries that fit beside the operand ring
+constexpr uint64_t kMatmulTimeoutNs = 2000000000ull;
+
+// mbar_wait_bounded for the matmul kernels: only a recorded time-out makes
+// other waits give up, so a call that reports bad offsets still completes its
+// good groups.
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                        uint64_t limit_ns = kMatmulTimeoutNs) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*reinterpret_cast<volatile uint32_t*>(err) & kErrWaitTimeout) return false;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        atomicOr(err, kErrWaitTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+// Rows [first, first + count) of group g; offsets == nullptr is one group of
+// all R rows.  A group whose offsets do not satisfy 0 <= o[g] <= o[g+1] <= R
+// counts as empty (*bad is set).
+__device__ __forceinline__ int group_rows(const int32_t* offsets, int g, int R, int* first,
+                                          bool* bad) {
+  if (offsets == nullptr) {
+    *first = 0;
+    return R;
+  }
+  const int lo = __ldg(offsets + g), hi = __ldg(offsets + g + 1);
+  *first = lo;
+  if (lo < 0 || hi < lo || hi > R) {
+    *first = 0;
+    *bad = true;
+    return 0;
+  }
+  return hi - lo;
+}
+
+// start[g] = units before group g when each group has ceil(rows / tile_m) * per
+// units; start[E] = their total.  Called by one warp.
+__device__ __forceinline__ void ragged_schedule(const int32_t* offsets, int E, int R, int tile_m,
+                                                int per, int* start, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int chunk = (E + 31) / 32;
+  const int g0 = min(E, lane * chunk), g1 = min(E, g0 + chunk);
+  bool bad = false;
+  int first, sum = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int mt = (group_rows(offsets, g, R, &first, &bad) + tile_m - 1) / tile_m;
+    start[g] = mt;
+    sum += mt;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  int run = inc - sum;
+  for (int g = g0; g < g1; ++g) {
+    const int mt = start[g];
+    start[g] = run * per;
+    run += mt;
+  }
+  if (lane == 31) start[E] = inc * per;
+  if (bad) atomicOr(status, kErrBadIndex);
+}
+
+// The group of unit u: start[g] <= u < start[g + 1].
+__device__ __forceinline__ int ragged_group(const int* start, int E, int u) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Shared-memory matrix descriptor of an operand stored with its contraction
+// index outermost: chunks of 128 bytes of the M (or N) index by 8 contraction
+// rows are 1024-byte swizzle atoms; the next 8 contraction rows follow at
+// 1024 bytes, the next 128 bytes of the M (or N) index at `chunk_bytes`.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(chunk_bytes >> 4) << 16;  // leading byte offset: next chunk along M / N
+  d |= (uint64_t)(1024u >> 4) << 32;        // stride byte offset: next 8 contraction rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Instruction-descriptor bits: operand stored contraction-outermost.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src,
+                                             int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+}  // namespace moe
