@@ -8,24 +8,41 @@
 // the input gradient) or outermost (W in the input gradient, dy and x in the
 // weight gradient), so no transposed copy of weights or rows exists.
 //
-// Work unit: a 128 x kBN output tile.  Forward and input gradient order the
-// units expert-major, then column tile, then row tile: CTAs running side by
-// side share a weight tile through L2 and each expert's weights stream from
-// HBM once.  The last column tile runs MMAs of its own width (rounded up to
-// 16) and loads only the 64-wide chunks it has; a row tile loads 32-row boxes
-// it has rows for, so a decode step's 1-row experts read 4 KB of rows per 32
-// KB of weights.  Rows of the next expert inside a box only reach output rows
+// Two SMs (a CTA pair, tcgen05 cta_group::2) compute one 256 x N tile.  Per
+// 64-wide K block each CTA stages its 128 of the tile's 256 M rows and half of
+// its N rows, 32 KB for 2 x 128 x 256 x 64 products: a third less traffic from
+// L2 and into shared memory than a 128 x 256 tile per CTA.
+//   forward, input gradient   M = 256 columns of the output (rows of W_e),
+//                             N = up to 256 of the expert's rows
+//   weight gradient           M = 256 rows of dW_e, N = 256 columns
+// The rows as N: an expert's rows are split into equal tiles of at most 256,
+// rounded up to 32, so a tile of few rows runs short MMAs and loads few rows
+// (an expert of 270 rows costs 320, as M it would cost 384).  The accumulator
+// then holds the output transposed (a TMEM lane is an output column); the
+// epilogue turns 32 x 32 blocks through shared memory.
+//
+// Forward and input gradient are fed from L2: a pair's K block of 256 x 256
+// moves 64 KB for 512 cycles of MMA, near what L2 gives 148 SMs at once, and a
+// tile of 144 rows moves 50 KB for 288.  So with enough units two row tiles of
+// an expert share one unit: each W block is staged once for both, and both
+// accumulators (256 TMEM columns each) are filled.
+//
+// Units are ordered expert-major, then M tile, then N tile: pairs running side
+// by side share weights and rows through L2, and each expert's weights stream
+// from HBM once.  Rows of the next expert inside a load only reach output rows
 // that are not stored.  The weight gradient contracts over the rows: in an
 // expert's last K block the rows past its end are overwritten with zeros in
 // shared memory (in both operands, as 0 * NaN is NaN) before the MMA reads them.
 //
-// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, then
-// the epilogue warps, which drain one accumulator (fp32, rounded once to bf16)
-// while the next tile accumulates in the other.  Full 32-row groups leave by
-// TMA stores of 64 columns, an expert's ragged last rows by row stores.
+// Roles per CTA: warp 0 TMA producer; warp 1 TMEM owner, in the pair's leader
+// MMA issuer, in its peer forwarding accumulator releases; warps 2-9 drain one
+// accumulator (fp32, rounded once to bf16) while the next tile accumulates in
+// the other; warp 10 (weight gradient) clears the rows past an expert's end.
 // Waits are bounded and set the status word when they give up.
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "epilogue.cuh"
 #include "internal.h"
@@ -35,337 +52,534 @@
 namespace moe {
 namespace {
 
-constexpr int GBM = 128, GBK = 64;
-constexpr int kChunkBytes = 64 * 64 * 2;  // 64 x 64 bf16 operand chunk
-constexpr int GABytes = GBM * GBK * 2;
-constexpr int GStg = 32 * 128;            // per epilogue warp: 32 rows x 64 bf16
+constexpr int GM = 256, GN = 256, GBK = 64;
+constexpr int kHalf = 128;                        // M rows (and at most N rows) of one CTA
+constexpr int kChunkBytes = 64 * GBK * 2;         // 64 x 64 operand chunk, contraction outermost
+constexpr int kHalfBytes = kHalf * GBK * 2;       // 16 KB
+constexpr int kEpiWarps = 8;
+constexpr int kStgBytes = 4096;                   // staging per epilogue warp (dw: two of them)
+constexpr uint32_t kTmemCols = 2 * GN;
 
 enum GMode { kFwd = 0, kDx = 1, kDw = 2 };
 
-template <int kBN>
-struct GCfg {
-  static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kStages = kBN == 256 ? 4 : 6;
-  static constexpr int kStageBytes = GABytes + kBN * GBK * 2;
-  static constexpr size_t smem(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kEpiWarps * GStg + 256 + (size_t)(E + 1) * 4;
-  }
-};
-static_assert(GCfg<256>::smem(kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
-static_assert(GCfg<128>::smem(kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
+constexpr int pair_threads(int mode) { return 64 + 32 * kEpiWarps + (mode == kDw ? 32 : 0); }
+// Operand ring: a stage holds one K block of a CTA's M half and of `share` N
+// halves; dw keeps one stage less for a second staging buffer per warp.
+__host__ __device__ constexpr int stage_bytes(int share) { return (1 + share) * kHalfBytes; }
+__host__ __device__ constexpr int stages(int mode, int share) {
+  return share == 2 ? 4 : mode == kDw ? 5 : 6;
+}
+__host__ __device__ constexpr int staging_bytes(int mode) {
+  return kEpiWarps * kStgBytes * (mode == kDw ? 2 : 1);
+}
+constexpr size_t pair_smem(int mode, int share, int E) {
+  return 1024 + (size_t)stages(mode, share) * stage_bytes(share) + staging_bytes(mode) + 256 +
+         (mode == kDw ? 0 : (size_t)(E + 1) * 4);
+}
+static_assert(pair_smem(kFwd, 1, kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
+static_assert(pair_smem(kFwd, 2, kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
+static_assert(pair_smem(kDw, 1, 0) <= 232448, "shared-memory opt-in");
 
 struct alignas(64) GArgs {
-  CUtensorMap tmA;    // fwd / dx: rows [R, K], box {64, 128}; dw: dy [R, n], box {64, 64}
-  CUtensorMap tmA32;  // fwd / dx: the same with box {64, 32}
-  CUtensorMap tmB;    // fwd / dx: W [E, n, k], box {64, 64, 1}; dw: x [R, k], box {64, 64}
-  CUtensorMap tmOut;  // fwd / dx: out [R, cols], box {64, 32}; dw: dW [E, n, k], box {64, 32, 1}
+  CUtensorMap tmM;    // fwd: W box {64, 128, 1}; dx: W box {64, 64, 1}; dw: dy box {64, 64}
+  CUtensorMap tmN;    // fwd, dx: rows box {64, 128}; dw: x box {64, 64}
+  CUtensorMap tmNs[3];  // fwd, dx: rows boxes {64, 16}, {64, 32}, {64, 64}
+  CUtensorMap tmOut;  // fwd, dx: out [R, m] box {32, 32}, not swizzled; dw: dW box {64, 32, 1}
   const int32_t* offsets;
   __nv_bfloat16* out;
   uint32_t* status;
   int E, R;
-  int m;     // dw: n (rows of dW_e); else unused
-  int cols;  // output columns
-  int kdim;  // fwd / dx: contraction length
+  int m;     // fwd, dx: output columns; dw: n
+  int cols;  // dw: k
+  int kdim;  // fwd, dx: contraction length
 };
 
-template <int kMode, int kBN>
-__global__ void __launch_bounds__(GCfg<kBN>::kThreads, 1) grouped_matmul_kernel(
+// Equal row tiles of an expert: at most 256 rows each, a multiple of 32.
+__device__ __forceinline__ int row_tile(int rows, int tiles) {
+  return ((rows + tiles - 1) / tiles + 31) & ~31;
+}
+
+// A CTA's N rows of one K block, `half` of them (a multiple of 16, at most
+// 128), in at most two copies: many copies of 16 rows each took 2-3x longer,
+// one box of the next size up moves up to 60% more than needed.
+struct RowBoxes {
+  int first, second;  // index of the box (16 << i rows), -1: none
+  __device__ __forceinline__ explicit RowBoxes(int half) {
+    first = half > 96 ? 3 : half > 64 || half == 64 ? 2 : half >= 32 ? 1 : 0;
+    const int left = half > 96 ? 0 : half - (16 << first);
+    second = left <= 0 ? -1 : left > 16 ? 1 : 0;
+  }
+  __device__ __forceinline__ int rows() const {
+    return (16 << first) + (second < 0 ? 0 : 16 << second);
+  }
+};
+
+// kShare: row tiles per unit (fwd, dx: 1 or 2; dw: 1)
+template <int kMode, int kShare>
+__global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_kernel(
     const __grid_constant__ GArgs args) {
-  using C = GCfg<kBN>;
-  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes;
+  constexpr int kStages = stages(kMode, kShare), kStageBytes = stage_bytes(kShare);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = base + (size_t)kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::kEpiWarps * GStg);
-  uint64_t* full = bars;
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;  // [2]
-  uint64_t* tempty = tfull + 2;       // [2]
-  uint64_t* drain = tempty + 2;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + staging_bytes(kMode));
+  uint64_t* full = bars;             // [kStages] leader: both CTAs' copies have landed
+  uint64_t* empty = full + kStages;    // [kStages] each CTA: the MMAs have read the stage
+  uint64_t* tfull = empty + kStages;   // [2] each CTA: accumulator complete
+  uint64_t* tempty = tfull + 2;      // [2] leader: the peer's epilogue has read it
+  uint64_t* edone = tempty + 2;      // [2] each CTA: its epilogue warps have read it
+  uint64_t* drain = edone + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  // dw: [kStages] each CTA: its last-block copies have landed; leader: cleared
+  uint64_t* tland = reinterpret_cast<uint64_t*>(tmem_holder) + 1;
+  uint64_t* tclear = tland + kStages;
   int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int NT = (args.cols + kBN - 1) / kBN;
-  const int MT = (args.m + GBM - 1) / GBM;  // dw
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int MT = (args.m + GM - 1) / GM;
+  const int NT = (args.cols + GN - 1) / GN;  // dw
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      if constexpr (kMode == kDw) {
+        mbar_init(&tland[s], 1);
+        mbar_init(&tclear[s], 2);
+      }
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], C::kEpiWarps);
+      mbar_init(&tempty[a], 1);
+      mbar_init(&edone[a], kEpiWarps);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, 2 * kBN);
-    tmem_relinquish();
+    tmem_alloc_2sm(tmem_holder, kTmemCols);
+    tmem_relinquish_2sm();
   }
   if constexpr (kMode != kDw) {
-    if (warp == 0) ragged_schedule(args.offsets, args.E, args.R, GBM, NT, start, args.status);
+    if (warp == 0)
+      ragged_schedule(args.offsets, args.E, args.R, kShare * GN, MT, start, args.status);
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int total = kMode == kDw ? args.E * MT * NT : start[args.E];
 
-  // unit -> expert g, its first row and row count, row tile m, column tile n
   struct Unit {
-    int g, first, rows, m, n, kb;
+    int g, first, rows;  // expert, its first row, its rows
+    int m0;              // first M index of the tile
+    int n0;              // first N index
+    int tiles;           // N tiles (accumulators): 1, or 2 (fwd, dx)
+    int width[2];        // N of each, a multiple of 32
+    int kb;              // K blocks
   };
   auto decode = [&](int u) {
     Unit t;
     bool bad = false;
+    t.tiles = 1;
+    t.width[1] = 0;
     if constexpr (kMode == kDw) {
       t.g = u / (MT * NT);
       const int local = u - t.g * (MT * NT);
-      t.m = local / NT;
-      t.n = local - t.m * NT;
+      const int m = local / NT;
+      t.m0 = m * GM;
+      t.n0 = (local - m * NT) * GN;
+      t.width[0] = min(GN, (args.cols - t.n0 + 31) & ~31);
       t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
       t.kb = (t.rows + GBK - 1) / GBK;
-      if (bad && t.m == 0 && t.n == 0) atomicOr(args.status, kErrBadIndex);
+      if (bad && local == 0 && tid == 0) atomicOr(args.status, kErrBadIndex);
     } else {
       t.g = ragged_group(start, args.E, u);
       t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
-      const int mt = (t.rows + GBM - 1) / GBM;
-      const int local = u - start[t.g];
-      t.n = local / mt;
-      t.m = local - t.n * mt;
+      const int tiles = (t.rows + GN - 1) / GN, local = u - start[t.g];
+      const int runs = (tiles + kShare - 1) / kShare;  // units per M tile
+      const int w = row_tile(t.rows, tiles), t0 = local % runs * kShare;
+      t.m0 = local / runs * GM;
+      t.n0 = t0 * w;
+      t.width[0] = min(w, (t.rows - t.n0 + 31) & ~31);
+      if (kShare == 2 && t0 + 1 < tiles) {
+        t.tiles = 2;
+        t.width[1] = min(w, (t.rows - t.n0 - w + 31) & ~31);
+      }
       t.kb = (args.kdim + GBK - 1) / GBK;
     }
     return t;
   };
+  // dw: the unit's last K block holds rows past the expert's end in its last
+  // 16-row step, which warp 10 clears
+  auto ragged_end = [&](const Unit& t) { return kMode == kDw && (t.rows & 15) != 0; };
 
   if (warp == 0) {
-    // ---- TMA producer ----
-    if (lane == 0) {
-      tma_prefetch_desc(&args.tmA);
-      tma_prefetch_desc(&args.tmB);
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, parity = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit t = decode(u);
-        const int nc = min(kBN / 64, (args.cols - t.n * kBN + 63) / 64);  // column chunks
-        const int rows = kMode == kDw ? args.m : t.rows;
-        const int left = rows - t.m * GBM;
-        // A: 64-wide chunks (dw) or 32-row boxes that hold rows of the tile
-        const int na = kMode == kDw ? (left > 64 ? 2 : 1) : min(4, (left + 31) / 32);
-        const uint32_t bytes =
-            (uint32_t)nc * kChunkBytes + (uint32_t)na * (kMode == kDw ? kChunkBytes : 32 * 128);
-        for (int kb = 0; kb < t.kb; ++kb) {
-          if (!mm_wait(&empty[stage], phase ^ 1u, args.status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = base + (size_t)stage * kStageBytes;
-          uint8_t* sb = sa + GABytes;
-          mbar_arrive_expect_tx(&full[stage], bytes);
+    // ---- TMA producer: like the MMA issuer, the warp walks the loop together
+    // and one lane issues ----
+    if (elect_one()) {
+      tma_prefetch_desc(&args.tmM);
+      tma_prefetch_desc(&args.tmN);
+    }
+    __syncwarp();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, parity = 0;
+    uint32_t tissued = 0, tphase = 0;  // last blocks: per stage, parity of the next use
+    bool ok = true;
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);  // the leader's barriers
+    Unit t = decode(pair < total ? pair : 0);
+    for (int u = pair; u < total && ok; u += npairs) {
+      const int mrow = t.m0 + (int)rank * kHalf;
+      Unit next = t;
+      if (t.kb == 0 && u + npairs < total) next = decode(u + npairs);
+      // dw: 64-wide chunks of this CTA's columns; fwd, dx: its rows of each tile
+      const int half = t.width[0] / 2, nrow = t.n0 + (int)rank * half;
+      const int nchunks = (half + 63) / 64;
+      const RowBoxes box0(half), box1(t.tiles == 2 ? t.width[1] / 2 : 16);
+      const int row0 = t.first + nrow;
+      const int row1 = t.first + t.n0 + t.width[0] + (int)rank * (t.width[1] / 2);
+      const uint32_t bytes =
+          kHalfBytes +
+          (uint32_t)(kMode == kDw
+                         ? nchunks * kChunkBytes
+                         : (box0.rows() + (t.tiles == 2 ? box1.rows() : 0)) * (GBK * 2));
+      for (int kb = 0; kb < t.kb; ++kb) {
+        ok = mm_wait(&empty[stage], phase ^ 1u, args.status);
+        if (!ok) break;
+        uint8_t* sm = base + (size_t)stage * kStageBytes;
+        uint8_t* sn = sm + kHalfBytes;
+        const uint32_t fbar = full0 + 8u * (uint32_t)stage;
+        const bool last = kb + 1 == t.kb && ragged_end(t);
+        if (elect_one()) {
           if constexpr (kMode == kDw) {
             const int r = t.first + kb * GBK;
-            for (int c = 0; c < na; ++c)
-              tma_load_2d(sa + c * kChunkBytes, &args.tmA, t.m * GBM + 64 * c, r, &full[stage]);
-            for (int c = 0; c < nc; ++c)
-              tma_load_2d(sb + c * kChunkBytes, &args.tmB, t.n * kBN + 64 * c, r, &full[stage]);
-          } else {
-            const int r = t.first + t.m * GBM;
-            if (na == 4) {
-              tma_load_2d(sa, &args.tmA, kb * GBK, r, &full[stage]);
+            if (last) {
+              // lands on this CTA's own barrier; `full` only advances
+              mbar_arrive_expect_tx(&tland[stage], bytes);
+              for (int c = 0; c < 2; ++c)
+                tma_load_2d(sm + c * kChunkBytes, &args.tmM, mrow + 64 * c, r, &tland[stage]);
+              for (int c = 0; c < nchunks; ++c)
+                tma_load_2d(sn + c * kChunkBytes, &args.tmN, nrow + 64 * c, r, &tland[stage]);
+              if (leader) mbar_arrive(&full[stage]);
             } else {
-              for (int c = 0; c < na; ++c)
-                tma_load_2d(sa + c * (32 * 128), &args.tmA32, kb * GBK, r + 32 * c, &full[stage]);
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+              for (int c = 0; c < 2; ++c)
+                tma_load_2d_2sm(sm + c * kChunkBytes, &args.tmM, mrow + 64 * c, r, fbar);
+              for (int c = 0; c < nchunks; ++c)
+                tma_load_2d_2sm(sn + c * kChunkBytes, &args.tmN, nrow + 64 * c, r, fbar);
             }
-            for (int c = 0; c < nc; ++c) {
-              const int col = t.n * kBN + 64 * c;
-              if constexpr (kMode == kFwd)
-                tma_load_3d(sb + c * kChunkBytes, &args.tmB, kb * GBK, col, t.g, &full[stage]);
-              else
-                tma_load_3d(sb + c * kChunkBytes, &args.tmB, col, kb * GBK, t.g, &full[stage]);
+          } else {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            if constexpr (kMode == kFwd) {
+              tma_load_3d_2sm(sm, &args.tmM, kb * GBK, mrow, t.g, fbar);
+            } else {
+              tma_load_3d_2sm(sm, &args.tmM, mrow, kb * GBK, t.g, fbar);
+              tma_load_3d_2sm(sm + kChunkBytes, &args.tmM, mrow + 64, kb * GBK, t.g, fbar);
             }
+            auto rows_in = [&](uint8_t* dst, const RowBoxes& box, int row) {
+              tma_load_2d_2sm(dst, box.first == 3 ? &args.tmN : &args.tmNs[box.first], kb * GBK,
+                              row, fbar);
+              if (box.second >= 0)
+                tma_load_2d_2sm(dst + (16 << box.first) * (GBK * 2), &args.tmNs[box.second],
+                                kb * GBK, row + (16 << box.first), fbar);
+            };
+            rows_in(sn, box0, row0);
+            if (kShare == 2 && t.tiles == 2) rows_in(sn + kHalfBytes, box1, row1);
           }
-          issued |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-      if (!ok) {  // let the copies already issued land before the CTA exits
-        for (int s = 0; s < kStages; ++s)
-          if ((issued >> s) & 1u)
-            mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
-      }
-    }
-  } else if (warp == 1) {
-    // ---- MMA issuer (the whole warp walks the loop; lane 0 issues) ----
-    constexpr uint32_t kMajor = (kMode == kDw ? kIdescAMn | kIdescBMn : 0u) |
-                                (kMode == kDx ? kIdescBMn : 0u);
-    int stage = 0;
-    uint32_t phase = 0;
-    int local = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++local) {
-      const Unit t = decode(u);
-      const int width = min(kBN, args.cols - t.n * kBN);
-      const uint32_t idesc = idesc_bf16_f32(GBM, (width + 15) / 16 * 16) | kMajor;
-      const int acc = local & 1;
-      if (!mm_wait(&tempty[acc], ((local >> 1) & 1) ^ 1u, args.status)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * kBN;
-      for (int kb = 0; kb < t.kb; ++kb) {
-        if (!mm_wait(&full[stage], phase, args.status)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sa = base + (size_t)stage * kStageBytes;
-        int steps = GBK / 16;
-        if constexpr (kMode == kDw) {
-          // rows of this K block that belong to the expert; the rest of the
-          // last 16-row step is zeroed: one 128-byte line per row and chunk
-          const int valid = t.rows - kb * GBK;
-          if (valid < GBK) {
-            steps = (valid + 15) / 16;
-            const int lines = steps * 16 - valid;
-            const int chunks = (GABytes + kBN * GBK * 2) / kChunkBytes;
-            for (int i = lane; i < lines * chunks * 8; i += 32) {
-              const int piece = i & 7, line = (i >> 3) % lines, c = (i >> 3) / lines;
-              *reinterpret_cast<uint4*>(sa + c * kChunkBytes + (valid + line) * 128 + piece * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sa), b0 = a0 + GABytes;
-#pragma unroll
-          for (int k = 0; k < GBK / 16; ++k) {
-            if (k < steps) {
-              const uint64_t ad = kMode == kDw ? smem_desc_mn_sw128(a0 + k * 2048, kChunkBytes)
-                                               : smem_desc_sw128(a0 + k * 32);
-              const uint64_t bd = kMode == kFwd ? smem_desc_sw128(b0 + k * 32)
-                                                : smem_desc_mn_sw128(b0 + k * 2048, kChunkBytes);
-              mma_bf16(d_tmem, ad, bd, idesc, (kb | k) != 0);
-            }
-          }
-          mma_commit(&empty[stage]);
         }
         __syncwarp();
+        if (last) {
+          tissued |= 1u << stage;
+          tphase ^= 1u << stage;
+        }
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
+        if (kb == 0 && u + npairs < total) next = decode(u + npairs);
       }
-      if (ok && lane == 0) mma_commit(&tfull[acc]);  // without K blocks: arrives at once
+      t = next;
+    }
+    if (!ok) {  // let the copies already issued land before the CTA exits
+      for (int s = 0; s < kStages; ++s) {
+        if (leader && ((issued >> s) & 1u))
+          mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
+        if (kMode == kDw && ((tissued >> s) & 1u))
+          mm_wait(&tland[s], ((tphase >> s) & 1u) ^ 1u, args.status, kMatmulTimeoutNs / 8);
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---- MMA issuer: the warp walks the loop together, so that addresses stay
+      // warp-uniform, and one lane issues ----
+      constexpr uint32_t kMajor = (kMode == kDx ? kIdescAMn : 0u) |
+                                  (kMode == kDw ? kIdescAMn | kIdescBMn : 0u);
+      constexpr bool kAInner = kMode == kFwd, kBInner = kMode != kDw;
+      const uint32_t ring = smem_u32(base);
+      const uint64_t ad0 = kAInner ? smem_desc_sw128(ring) : smem_desc_mn_sw128(ring, kChunkBytes);
+      const uint64_t bd0 = kBInner ? smem_desc_sw128(ring + kHalfBytes)
+                                   : smem_desc_mn_sw128(ring + kHalfBytes, kChunkBytes);
+      const uint32_t a_hi = desc_hi(ad0), b_hi = desc_hi(bd0);
+      constexpr uint32_t kAStep = (kAInner ? 32 : 2048) / 16, kBStep = (kBInner ? 32 : 2048) / 16;
+      int stage = 0;
+      uint32_t phase = 0, tphase = 0;
+      int use = 0;  // accumulator uses so far
+      bool ok = true;
+      Unit t = decode(pair < total ? pair : 0);
+      for (int u = pair; u < total && ok; u += npairs) {
+        for (int j = 0; j < t.tiles && ok; ++j) {
+          const uint32_t ap = (((use + j) >> 1) & 1) ^ 1u;
+          ok = mm_wait(&edone[(use + j) & 1], ap, args.status) &&
+               mm_wait<true>(&tempty[(use + j) & 1], ap, args.status);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        Unit next = t;
+        if (t.kb == 0 && u + npairs < total) next = decode(u + npairs);
+        for (int kb = 0; kb < t.kb && ok; ++kb) {
+          int steps = GBK / 16;
+          if constexpr (kMode == kDw) {
+            if (kb + 1 == t.kb) {
+              steps = (t.rows - kb * GBK + 15) / 16;
+              if (ragged_end(t)) {
+                ok = mm_wait<true>(&tclear[stage], (tphase >> stage) & 1u, args.status);
+                if (!ok) break;
+                tphase ^= 1u << stage;
+              }
+            }
+          }
+          ok = mm_wait(&full[stage], phase, args.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t off = (uint32_t)stage * (kStageBytes / 16);
+          const uint32_t a_lo = desc_lo(ad0) + off, b_lo = desc_lo(bd0) + off;
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < kShare; ++j) {
+              if (j >= t.tiles) break;
+              const uint32_t idesc = idesc_bf16_f32(GM, t.width[j]) | kMajor;
+              const uint32_t d_tmem = tmem_base + ((use + j) & 1) * GN;
+#pragma unroll
+              for (int k = 0; k < GBK / 16; ++k)
+                if (kMode != kDw || k < steps)
+                  mma_bf16_2sm_parts(d_tmem, a_lo + k * kAStep, a_hi,
+                                     b_lo + j * (kHalfBytes / 16) + k * kBStep, b_hi, idesc,
+                                     k == 0 ? (uint32_t)(kb != 0) : 1u);
+            }
+            mma_commit_2sm_mc(&empty[stage], 0x3);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          // the next unit is looked up while this one's products run
+          if (kb == 0 && u + npairs < total) next = decode(u + npairs);
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          for (int j = 0; j < t.tiles; ++j)  // without K blocks: arrives at once
+            mma_commit_2sm_mc(&tfull[(use + j) & 1], 0x3);
+        }
+        __syncwarp();
+        use += t.tiles;
+        t = next;
+      }
+      if (elect_one()) {
+        mma_commit_2sm(drain);
+        mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
+      }
       __syncwarp();
+    } else if (!leader && lane == 0) {
+      // forward each accumulator release of this CTA's epilogue to the leader
+      const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+      int use = 0;
+      bool ok = true;
+      for (int u = pair; u < total && ok; u += npairs) {
+        const Unit t = decode(u);
+        for (int j = 0; j < t.tiles && ok; ++j, ++use) {
+          ok = mm_wait(&edone[use & 1], (use >> 1) & 1, args.status);
+          if (ok) mbar_arrive_cluster(tempty0 + 8u * (uint32_t)(use & 1));
+        }
+      }
     }
-    if (lane == 0) {
-      mma_commit(drain);
-      mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
-    }
-    __syncwarp();
-  } else {
-    // ---- epilogue: two warps per TMEM lane quadrant, kBN / 2 columns each ----
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stg = staging + (size_t)(warp - 2) * GStg;
-    int local = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++local) {
+  } else if (kMode == kDw && warp == 2 + kEpiWarps) {
+    // ---- rows past an expert's end, in its last 16-row step: one 128-byte line
+    // per row and 64-wide chunk ----
+    int kbs = 0;  // K blocks of the units so far
+    uint32_t tphase = 0;
+    const uint32_t tclear0 = mapa_shared(smem_u32(&tclear[0]), 0);
+    for (int u = pair; u < total; u += npairs) {
       const Unit t = decode(u);
-      const int acc = local & 1;
-      if (!mm_wait(&tfull[acc], (local >> 1) & 1, args.status)) break;
-      tc_fence_after();
-      const int r0 = t.m * GBM + q * 32;  // this warp's first row of the group (of dW_e)
-      const int left = (kMode == kDw ? args.m : t.rows) - r0;
-      const bool by_tma = kMode == kDw || left >= 32;
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kBN;
-#pragma unroll 1
-      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 64) {
-        const int col = t.n * kBN + c;
-        if (left <= 0 || col >= args.cols) break;  // warp-uniform
-        uint32_t p[32];
-        if (kMode == kDw && t.kb == 0) {  // an expert without rows: a zero gradient
-#pragma unroll
-          for (int i = 0; i < 32; ++i) p[i] = 0u;
-        } else {
-          uint32_t v0[32], v1[32];
-          tmem_ld32(taddr + c, v0);
-          tmem_ld32(taddr + c + 32, v1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            p[i] = bf16x2_bits(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1]));
-            p[16 + i] = bf16x2_bits(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1]));
-          }
-        }
-        if (by_tma) {
-          if (lane == 0) bulk_wait_read_all();  // the previous piece has left the buffer
-          __syncwarp();
-          uint8_t* my = stg + lane * 128;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(my + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (kMode == kDw)
-              tma_store_3d(&args.tmOut, stg, col, r0, t.g);
-            else
-              tma_store_2d(&args.tmOut, stg, col, t.first + r0);
-            bulk_commit_group();
-          }
-        } else if (lane < left) {
-          __nv_bfloat16* dst =
-              args.out + (size_t)(t.first + r0 + lane) * (size_t)args.cols + col;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (col + 8 * j < args.cols)
-              reinterpret_cast<uint4*>(dst)[j] =
-                  make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-        }
+      kbs += t.kb;
+      if (!ragged_end(t)) continue;
+      const int stage = (kbs - 1) % kStages;
+      if (!mm_wait(&tland[stage], (tphase >> stage) & 1u, args.status)) break;
+      tphase ^= 1u << stage;
+      uint8_t* sm = base + (size_t)stage * kStageBytes;
+      const int valid = t.rows - (t.kb - 1) * GBK, lines = ((valid + 15) & ~15) - valid;
+      for (int i = lane; i < lines * (kStageBytes / kChunkBytes) * 8; i += 32) {
+        const int piece = i & 7, line = (i >> 3) % lines, c = (i >> 3) / lines;
+        *reinterpret_cast<uint4*>(sm + c * kChunkBytes + (valid + line) * 128 + piece * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
       }
-      tc_fence_before();
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (lane == 0) mbar_arrive_cluster(tclear0 + 8u * (uint32_t)stage);
     }
-    if (lane == 0) bulk_wait_all();  // the staging buffer outlives the stores that read it
+  } else {
+    // ---- epilogue ----
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quadrant; two warps each
+    uint8_t* stg = staging + (size_t)(warp - 2) * (staging_bytes(kMode) / kEpiWarps);
+    int use = 0, buf = 0;
+    bool ok = true;
+    for (int u = pair; u < total && ok; u += npairs) {
+      const Unit t = decode(u);
+      const int m = t.m0 + (int)rank * kHalf + q * 32;  // this warp's first M index
+      for (int j = 0; j < t.tiles; ++j, ++use) {
+        const int acc = use & 1;
+        ok = mm_wait(&tfull[acc], (use >> 1) & 1, args.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * GN;
+        if (kMode == kDw && m < args.m) {
+          // 32 rows of dW_e, 64 columns at a time
+#pragma unroll 1
+          for (int c = half * 128; c < half * 128 + 128; c += 64, buf ^= 1) {
+            if (t.n0 + c >= args.cols) break;
+            uint32_t p[32];
+            if (t.kb == 0) {  // an expert without rows: a zero gradient
+#pragma unroll
+              for (int i = 0; i < 32; ++i) p[i] = 0u;
+            } else {
+              uint32_t v0[32], v1[32];
+              tmem_ld32(taddr + c, v0);
+              tmem_ld32(taddr + c + 32, v1);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                p[i] = bf16x2_bits(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1]));
+                p[16 + i] =
+                    bf16x2_bits(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1]));
+              }
+            }
+            uint8_t* tile = stg + buf * kStgBytes;
+            if (lane == 0) bulk_wait_read_but_one();  // this buffer's last store has read it
+            __syncwarp();
+            uint8_t* my = tile + lane * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(my + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&args.tmOut, tile, t.n0 + c, m, t.g);
+              bulk_commit_group();
+            }
+          }
+        }
+        if (kMode != kDw && m < args.m) {
+          // lane = output column m + lane, register = row: blocks of 32 rows,
+          // alternately by the two warps of a quadrant, turned in the staging
+          // buffer (row i at 64 i, column at 2 lane)
+          const int n0 = t.n0 + (j == 0 ? 0 : t.width[0]);
+          const int width = t.width[j];
+#pragma unroll 1
+          for (int b = half * 32; b < width; b += 64, buf ^= 1) {
+            const int left = t.rows - n0 - b;
+            if (left <= 0) break;
+            uint32_t v[32];
+            tmem_ld32(taddr + b, v);
+            tmem_wait_ld();
+            uint8_t* tile = stg + buf * 2048;
+            if (lane == 0) bulk_wait_read_but_one();  // this buffer's last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              *reinterpret_cast<__nv_bfloat16*>(tile + i * 64 + lane * 2) =
+                  __float2bfloat16_rn(__uint_as_float(v[i]));
+            const int r = t.first + n0 + b;
+            if (left >= 32) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&args.tmOut, tile, m, r);
+                bulk_commit_group();
+              }
+            } else {
+              // the expert's last rows: 16 bytes a lane, 8 rows at a time
+              __syncwarp();
+              const int c = (lane & 3) * 8;
+              for (int i = lane >> 2; i < left; i += 8)
+                if (m + c < args.m)
+                  *reinterpret_cast<uint4*>(args.out + (size_t)(r + i) * (size_t)args.m + m + c) =
+                      *reinterpret_cast<const uint4*>(tile + i * 64 + c * 2);
+              __syncwarp();
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&edone[acc]);
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // the staging buffers outlive the stores that read them
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 2 * kBN);
+    tmem_dealloc_2sm(tmem_base, kTmemCols);
   }
 }
 
-template <int kMode, int kBN>
-cudaError_t launch(const GArgs& a, long long units, cudaStream_t st) {
-  const size_t smem = GCfg<kBN>::smem(a.E);
-  auto kernel = grouped_matmul_kernel<kMode, kBN>;
+template <int kMode, int kShare>
+cudaError_t launch_pair(const GArgs& a, long long units, cudaStream_t st) {
+  auto kernel = grouped_matmul_pair_kernel<kMode, kShare>;
+  const size_t smem = pair_smem(kMode, kShare, a.E);
   cudaError_t e =
       note_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)smem),
+                                     (int)pair_smem(kMode, kShare, kMatmulMaxGroups)),
                 "grouped matmul: set shared-memory size");
   if (e != cudaSuccess) return e;
-  const int grid = (int)(units < num_sms() ? units : num_sms());
-  kernel<<<grid, GCfg<kBN>::kThreads, smem, st>>>(a);
-  return note_cuda(cudaGetLastError(), "grouped matmul launch");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(pair_threads(kMode), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(num_sms() & ~1), 1, 1);
+  // as many pairs as can be resident at once (one CTA per SM whatever E is)
+  static std::atomic<int> resident{0};
+  int pairs = resident.load();
+  if (pairs == 0) {
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0)
+      pairs = num_sms() / 2;
+    resident.store(pairs);
+  }
+  if (units < pairs) pairs = (int)units;
+  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  return note_cuda(cudaLaunchKernelEx(&cfg, kernel, a), "grouped matmul launch");
 }
 
 }  // namespace
 
-// mode 0: rows = x [R, k], out = y [R, n]; 1: rows = dy [R, n], out = dx [R, k];
-// w [E, n, k], bf16, n and k multiples of 8.
 int launch_grouped_matmul_bf16(int mode, const void* rows, int R, const int32_t* offsets, int E,
                                const void* w, int n, int k, void* out, void* ws,
                                cudaStream_t st) {
@@ -376,26 +590,30 @@ int launch_grouped_matmul_bf16(int mode, const void* rows, int R, const int32_t*
   a.status = static_cast<uint32_t*>(ws);
   a.E = E;
   a.R = R;
-  a.cols = mode == kDx ? k : n;
+  a.m = mode == kDx ? k : n;
   a.kdim = mode == kDx ? n : k;
   const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E};
   const uint64_t strides[2] = {(uint64_t)k * 2, (uint64_t)k * n * 2};
-  const uint32_t box[3] = {64, 64, 1};
-  if (!make_map(&a.tmA, rows, BF, 2, a.kdim, R, 64, 128) ||
-      !make_map(&a.tmA32, rows, BF, 2, a.kdim, R, 64, 32) ||
-      !make_map_nd(&a.tmB, w, BF, 3, dims, strides, box) ||
-      !make_map_swizzled(&a.tmOut, out, BF, 2, a.cols, R, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) {
+  const uint32_t box[3] = {64, mode == kDx ? 64u : 128u, 1};
+  if (!make_map_nd(&a.tmM, w, BF, 3, dims, strides, box) ||
+      !make_map(&a.tmN, rows, BF, 2, a.kdim, R, 64, 128) ||
+      !make_map(&a.tmNs[0], rows, BF, 2, a.kdim, R, 64, 16) ||
+      !make_map(&a.tmNs[1], rows, BF, 2, a.kdim, R, 64, 32) ||
+      !make_map(&a.tmNs[2], rows, BF, 2, a.kdim, R, 64, 64) ||
+      !make_map_swizzled(&a.tmOut, out, BF, 2, a.m, R, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) {
     note_text("grouped matmul: tensor-map encoding failed");
     return MOE_ERR_CUDA;
   }
-  const long long mt = R / GBM + (R < E ? R : E);  // no more row tiles than this
-  const long long units = mt * ((a.cols + 255) / 256);
+  const long long tiles = R / GN + (R < E ? R : E);  // no more row tiles than this
+  const long long units = tiles * ((a.m + GM - 1) / GM);
+  const bool share = units >= 8 * (num_sms() / 2);
   const cudaError_t e =
-      mode == kFwd ? launch<kFwd, 256>(a, units, st) : launch<kDx, 256>(a, units, st);
+      mode == kFwd
+          ? (share ? launch_pair<kFwd, 2>(a, units, st) : launch_pair<kFwd, 1>(a, units, st))
+          : (share ? launch_pair<kDx, 2>(a, units, st) : launch_pair<kDx, 1>(a, units, st));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// dw [E, n, k] from dy [R, n] and x [R, k], bf16, n and k multiples of 8.
 int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const int32_t* offsets,
                                   int E, int n, int k, void* dw, void* ws, cudaStream_t st) {
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -410,13 +628,13 @@ int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const in
   const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E};
   const uint64_t strides[2] = {(uint64_t)k * 2, (uint64_t)k * n * 2};
   const uint32_t box[3] = {64, 32, 1};
-  if (!make_map(&a.tmA, dy, BF, 2, n, R, 64, 64) || !make_map(&a.tmB, x, BF, 2, k, R, 64, 64) ||
+  if (!make_map(&a.tmM, dy, BF, 2, n, R, 64, 64) || !make_map(&a.tmN, x, BF, 2, k, R, 64, 64) ||
       !make_map_nd(&a.tmOut, dw, BF, 3, dims, strides, box)) {
     note_text("grouped matmul weight gradient: tensor-map encoding failed");
     return MOE_ERR_CUDA;
   }
-  const long long units = (long long)E * ((n + GBM - 1) / GBM) * ((k + 255) / 256);
-  return launch<kDw, 256>(a, units, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const long long units = (long long)E * ((n + GM - 1) / GM) * ((k + GN - 1) / GN);
+  return launch_pair<kDw, 1>(a, units, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

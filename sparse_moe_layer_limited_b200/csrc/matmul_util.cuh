@@ -13,16 +13,23 @@ constexpr uint64_t kMatmulTimeoutNs = 2000000000ull;
 
 // mbar_wait_bounded for the matmul kernels: only a recorded time-out makes
 // other waits give up, so a call that reports bad offsets still completes its
-// good groups.
+// good groups; and the clock is first read after 64 tries, as reading it on
+// every wait that does not succeed at once delays the pipeline.  kCluster:
+// cluster-scope acquire, for barriers the peer CTA arrives on.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                         uint64_t limit_ns = kMatmulTimeoutNs) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  auto ready = [&] {
+    return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  };
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0) {
+    if (ready()) return true;
+    if ((it & 63u) == 0) {
       if (*reinterpret_cast<volatile uint32_t*>(err) & kErrWaitTimeout) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
         atomicOr(err, kErrWaitTimeout);
         return false;
       }
@@ -105,12 +112,48 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 // Instruction-descriptor bits: operand stored contraction-outermost.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
+
+// The two 32-bit halves of a descriptor: only the low one changes as a kernel
+// walks its ring and the contraction steps (addresses count 16-byte units).
+__device__ __forceinline__ uint32_t desc_lo(uint64_t d) { return (uint32_t)d; }
+__device__ __forceinline__ uint32_t desc_hi(uint64_t d) { return (uint32_t)(d >> 32); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void mma_bf16_2sm_parts(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi,
+                                                   uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, int32_t z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// The same, completing on the pair leader's barrier (see tma_load_2d_2sm).
+__device__ __forceinline__ void tma_load_3d_2sm(void* smem_dst, const CUtensorMap* map, int32_t x,
+                                                int32_t y, int32_t z, uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src,
