@@ -411,55 +411,72 @@ def moe_forward(s, x, router_w, bias, gamma, w13, w2, w13_scales, w2_scales, top
 # ---- products by expert and layer norm ------------------------------------------------
 # These calls read their sizes from the tensors and launch on the tensors' own
 # device, whichever device is current; all tensors of a call must share it.
+# Their smallest launches take a few microseconds, so the checks are kept short.
 
 _DTYPES = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16}
 _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 
 
-def _tensor(t, name, dtype, shape, like):
-    """The data pointer of a contiguous CUDA tensor of this dtype and shape on
-    the device of `like`."""
-    if t.dtype != dtype:
+def _tensor(t, name, dtype, shape, dev):
+    """The data pointer of a contiguous tensor of this dtype and shape on the
+    CUDA device with index `dev`."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, but the call runs on {like.device}")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    return t.data_ptr()
 
 
-def _scratch(t, name, size, like):
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, but the call runs on {like.device}")
-    if t.numel() * t.element_size() < size:
-        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, needs {size}")
-    return _ptr(t)
+def _scratch(t, name, size, dev):
+    if t.nbytes < size:
+        raise ValueError(f"{name}: {t.nbytes} bytes, needs {size}")
+    return _tensor(t, name, t.dtype, t.shape, dev)
 
 
 def _matrix(t, name, dims):
-    if t.dim() != dims:
-        raise ValueError(f"{name}: expected {dims} dimensions, got {t.dim()}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got {len(shape)}")
+    return shape
 
 
-def _offsets(offsets, experts, like):
+def _device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must live on the GPU")
+    return t.get_device()
+
+
+def _offsets(offsets, experts, dev):
     if offsets is None:
         if experts != 1:
             raise ValueError("offsets: required for more than one expert")
         return None
-    return _tensor(offsets, "offsets", torch.int32, (experts + 1,), like)
+    return _tensor(offsets, "offsets", torch.int32, (experts + 1,), dev)
 
 
-def _call_on(t, name, stream, *args):
-    """The C call on t's device: its current stream, or `stream`."""
-    dev = t.device
+_fns = {}
+
+
+def _call_on(dev, name, stream, *args):
+    """The C call on device `dev`: its current stream, or `stream`."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        _call(name, *args, _stream(stream))
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _call(name, *args, _stream(stream))
+            rc = fn(*args, stream)
+    if rc != OK:
+        raise MoEError(name, rc)
 
 
 def matmul_workspace_size() -> int:
@@ -471,9 +488,10 @@ def layer_norm_workspace_size(rows, d) -> int:
 
 
 def _mm_dtype(t, name):
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return dt
 
 
 def moe_grouped_matmul(x, offsets, w, y, ws, stream=None):
@@ -483,10 +501,10 @@ def moe_grouped_matmul(x, offsets, w, y, ws, stream=None):
     offsets[0] .. offsets[-1] of y are left as they were."""
     E, n, k = _matrix(w, "w", 3)
     R = _matrix(x, "x", 2)[0]
-    dt = _mm_dtype(x, "x")
-    _call_on(x, "moe_grouped_matmul", stream, _tensor(x, "x", x.dtype, (R, k), x), R,
-             _offsets(offsets, E, x), E, _tensor(w, "w", x.dtype, (E, n, k), x), n, k, dt,
-             _tensor(y, "y", x.dtype, (R, n), x), _scratch(ws, "ws", 256, x))
+    t, dt, dev = x.dtype, _mm_dtype(x, "x"), _device(x, "x")
+    _call_on(dev, "moe_grouped_matmul", stream, _tensor(x, "x", t, (R, k), dev), R,
+             _offsets(offsets, E, dev), E, _tensor(w, "w", t, (E, n, k), dev), n, k, dt,
+             _tensor(y, "y", t, (R, n), dev), _scratch(ws, "ws", 256, dev))
 
 
 def moe_grouped_matmul_dx(dy, offsets, w, dx, ws, stream=None):
@@ -494,10 +512,10 @@ def moe_grouped_matmul_dx(dy, offsets, w, dx, ws, stream=None):
     [rows, n], dx [rows, k])."""
     E, n, k = _matrix(w, "w", 3)
     R = _matrix(dy, "dy", 2)[0]
-    dt = _mm_dtype(dy, "dy")
-    _call_on(dy, "moe_grouped_matmul_dx", stream, _tensor(dy, "dy", dy.dtype, (R, n), dy), R,
-             _offsets(offsets, E, dy), E, _tensor(w, "w", dy.dtype, (E, n, k), dy), n, k, dt,
-             _tensor(dx, "dx", dy.dtype, (R, k), dy), _scratch(ws, "ws", 256, dy))
+    t, dt, dev = dy.dtype, _mm_dtype(dy, "dy"), _device(dy, "dy")
+    _call_on(dev, "moe_grouped_matmul_dx", stream, _tensor(dy, "dy", t, (R, n), dev), R,
+             _offsets(offsets, E, dev), E, _tensor(w, "w", t, (E, n, k), dev), n, k, dt,
+             _tensor(dx, "dx", t, (R, k), dev), _scratch(ws, "ws", 256, dev))
 
 
 def moe_grouped_matmul_dw(dy, x, offsets, dw, ws, stream=None):
@@ -505,55 +523,53 @@ def moe_grouped_matmul_dw(dy, x, offsets, dw, ws, stream=None):
     moe_grouped_matmul (dw [experts, n, k]; zeros for an expert without rows)."""
     E, n, k = _matrix(dw, "dw", 3)
     R = _matrix(dy, "dy", 2)[0]
-    dt = _mm_dtype(dy, "dy")
-    _call_on(dy, "moe_grouped_matmul_dw", stream, _tensor(dy, "dy", dy.dtype, (R, n), dy),
-             _tensor(x, "x", dy.dtype, (R, k), dy), R, _offsets(offsets, E, dy), E, n, k, dt,
-             _tensor(dw, "dw", dy.dtype, (E, n, k), dy), _scratch(ws, "ws", 256, dy))
+    t, dt, dev = dy.dtype, _mm_dtype(dy, "dy"), _device(dy, "dy")
+    _call_on(dev, "moe_grouped_matmul_dw", stream, _tensor(dy, "dy", t, (R, n), dev),
+             _tensor(x, "x", t, (R, k), dev), R, _offsets(offsets, E, dev), E, n, k, dt,
+             _tensor(dw, "dw", t, (E, n, k), dev), _scratch(ws, "ws", 256, dev))
 
 
 def _fp8_format(t, name):
-    if t.dtype not in _FP8:
+    fmt = _FP8.get(t.dtype)
+    if fmt is None:
         raise TypeError(f"{name}: expected float8_e4m3fn or float8_e5m2, got {t.dtype}")
-    return _FP8[t.dtype]
-
-
-def _row_scales(scales, name, cols, like):
-    blocks, ld = _matrix(scales, name, 2)
-    return _tensor(scales, name, torch.float32, (-(-cols // 128), ld), like), ld
+    return fmt
 
 
 def moe_quantize_rows_fp8(x, codes, scales, stream=None):
     """x [rows, cols] bf16 -> codes [rows, cols] (float8_e4m3fn or float8_e5m2,
     by the tensor's dtype) and scales [ceil(cols / 128), ld >= rows] fp32."""
     R, C = _matrix(x, "x", 2)
-    fmt = _fp8_format(codes, "codes")
-    sp, ld = _row_scales(scales, "scales", C, x)
-    _call_on(x, "moe_quantize_rows_fp8", stream, _tensor(x, "x", torch.bfloat16, (R, C), x), R, C,
-             fmt, _tensor(codes, "codes", codes.dtype, (R, C), x), sp, ld)
+    fmt, dev = _fp8_format(codes, "codes"), _device(x, "x")
+    ld = _matrix(scales, "scales", 2)[1]
+    _call_on(dev, "moe_quantize_rows_fp8", stream, _tensor(x, "x", torch.bfloat16, (R, C), dev), R,
+             C, fmt, _tensor(codes, "codes", codes.dtype, (R, C), dev),
+             _tensor(scales, "scales", torch.float32, (-(-C // 128), ld), dev), ld)
 
 
 def moe_quantize_blocks_fp8(w, codes, scales, stream=None):
     """w [experts, n, k] bf16 -> codes float8_e4m3fn [experts, n, k] and scales
     fp32 [experts, ceil(n / 128), ceil(k / 128)], one per 128x128 block."""
     E, n, k = _matrix(w, "w", 3)
-    _call_on(w, "moe_quantize_blocks_fp8", stream,
-             _tensor(w, "w", torch.bfloat16, (E, n, k), w), E, n, k,
-             _tensor(codes, "codes", torch.float8_e4m3fn, (E, n, k), w),
-             _tensor(scales, "scales", torch.float32, (E, -(-n // 128), -(-k // 128)), w))
+    dev = _device(w, "w")
+    _call_on(dev, "moe_quantize_blocks_fp8", stream,
+             _tensor(w, "w", torch.bfloat16, (E, n, k), dev), E, n, k,
+             _tensor(codes, "codes", torch.float8_e4m3fn, (E, n, k), dev),
+             _tensor(scales, "scales", torch.float32, (E, -(-n // 128), -(-k // 128)), dev))
 
 
 def _matmul_fp8(name, rows, scales, offsets, w, w_scales, out, ws, stream, dx):
     E, n, k = _matrix(w, "w", 3)
     R = _matrix(rows, "codes", 2)[0]
-    fmt = _fp8_format(rows, "codes")
+    fmt, dev = _fp8_format(rows, "codes"), _device(rows, "codes")
     cin, cout = (n, k) if dx else (k, n)
-    sp, ld = _row_scales(scales, "scales", cin, rows)
-    _call_on(rows, name, stream, _tensor(rows, "codes", rows.dtype, (R, cin), rows), fmt, sp, ld,
-             R, _offsets(offsets, E, rows), E,
-             _tensor(w, "w", torch.float8_e4m3fn, (E, n, k), rows),
-             _tensor(w_scales, "w_scales", torch.float32, (E, -(-n // 128), -(-k // 128)), rows),
-             n, k, _tensor(out, "out", torch.bfloat16, (R, cout), rows),
-             _scratch(ws, "ws", 256, rows))
+    ld = _matrix(scales, "scales", 2)[1]
+    f32 = torch.float32
+    _call_on(dev, name, stream, _tensor(rows, "codes", rows.dtype, (R, cin), dev), fmt,
+             _tensor(scales, "scales", f32, (-(-cin // 128), ld), dev), ld, R,
+             _offsets(offsets, E, dev), E, _tensor(w, "w", torch.float8_e4m3fn, (E, n, k), dev),
+             _tensor(w_scales, "w_scales", f32, (E, -(-n // 128), -(-k // 128)), dev), n, k,
+             _tensor(out, "out", torch.bfloat16, (R, cout), dev), _scratch(ws, "ws", 256, dev))
 
 
 def moe_matmul_fp8(x, x_scales, offsets, w, w_scales, y, ws, stream=None):
@@ -576,24 +592,22 @@ def moe_layer_norm(x, weight, bias, eps, y, mean, rstd, stream=None):
     [rows, d] (bf16 or fp32; weight, bias fp32 [d], bias may be None); writes
     the rows' mean and rstd (fp32 [rows]) for the backward."""
     R, d = _matrix(x, "x", 2)
-    dt = _mm_dtype(x, "x")
-    f32 = torch.float32
-    _call_on(x, "moe_layer_norm", stream, _tensor(x, "x", x.dtype, (R, d), x),
-             _tensor(weight, "weight", f32, (d,), x),
-             None if bias is None else _tensor(bias, "bias", f32, (d,), x), eps, R, d, dt,
-             _tensor(y, "y", x.dtype, (R, d), x), _tensor(mean, "mean", f32, (R,), x),
-             _tensor(rstd, "rstd", f32, (R,), x))
+    t, dt, dev, f32 = x.dtype, _mm_dtype(x, "x"), _device(x, "x"), torch.float32
+    _call_on(dev, "moe_layer_norm", stream, _tensor(x, "x", t, (R, d), dev),
+             _tensor(weight, "weight", f32, (d,), dev),
+             None if bias is None else _tensor(bias, "bias", f32, (d,), dev), eps, R, d, dt,
+             _tensor(y, "y", t, (R, d), dev), _tensor(mean, "mean", f32, (R,), dev),
+             _tensor(rstd, "rstd", f32, (R,), dev))
 
 
 def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None):
     """Gradients of moe_layer_norm: dx [rows, d] in x's type, dweight and dbias
     fp32 [d] (dbias may be None).  ws: layer_norm_workspace_size(rows, d) bytes."""
     R, d = _matrix(x, "x", 2)
-    dt = _mm_dtype(x, "x")
-    f32 = torch.float32
-    _call_on(x, "moe_layer_norm_backward", stream, _tensor(dy, "dy", x.dtype, (R, d), x),
-             _tensor(x, "x", x.dtype, (R, d), x), _tensor(weight, "weight", f32, (d,), x),
-             _tensor(mean, "mean", f32, (R,), x), _tensor(rstd, "rstd", f32, (R,), x), R, d, dt,
-             _tensor(dx, "dx", x.dtype, (R, d), x), _tensor(dweight, "dweight", f32, (d,), x),
-             None if dbias is None else _tensor(dbias, "dbias", f32, (d,), x),
-             _scratch(ws, "ws", layer_norm_workspace_size(R, d), x))
+    t, dt, dev, f32 = x.dtype, _mm_dtype(x, "x"), _device(x, "x"), torch.float32
+    _call_on(dev, "moe_layer_norm_backward", stream, _tensor(dy, "dy", t, (R, d), dev),
+             _tensor(x, "x", t, (R, d), dev), _tensor(weight, "weight", f32, (d,), dev),
+             _tensor(mean, "mean", f32, (R,), dev), _tensor(rstd, "rstd", f32, (R,), dev), R, d,
+             dt, _tensor(dx, "dx", t, (R, d), dev), _tensor(dweight, "dweight", f32, (d,), dev),
+             None if dbias is None else _tensor(dbias, "dbias", f32, (d,), dev),
+             _scratch(ws, "ws", layer_norm_workspace_size(R, d), dev))

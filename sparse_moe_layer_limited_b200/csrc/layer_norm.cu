@@ -4,15 +4,20 @@
 //   h    = dy w,  z = (x - mean) rstd
 //   dx   = rstd (h - mean(h) - z mean(h z)),  dw = sum_rows dy z,  db = sum_rows dy
 //
-// Both passes are bound by HBM: a row is read once into registers, reduced,
-// and written.  kT threads share a row (a warp up to 1024 columns, then 128,
-// 256 or 512 threads); each holds up to 32 of its elements, in 16-byte pieces
-// when the rows are 16-byte aligned, else one by one.  The next row's loads are
-// issued before the current row is reduced.
+// Both passes are bound by HBM: a row is read once, reduced, and written.
+//   up to 1024 columns   a warp per row, up to 32 elements a lane in registers,
+//                        the next row loaded while the current one is reduced
+//   wider, rows in whole 16-byte pieces (row_kernel, row_bwd_kernel): a CTA of
+//                        one thread per two pieces works on two rows at a time,
+//                        with one block barrier; each thread copies its own pieces
+//                        of the next four rows asynchronously into shared memory,
+//                        which keeps 115 KB in flight per SM (backward, 7168
+//                        columns) without registers
+//   other widths         128 to 512 threads a row, elements in registers
 //
 // Statistics: each thread takes the mean and the centred square sum of its own
-// elements, and pairs (count, mean, M2) are merged by Chan's update, so one
-// block-wide exchange suffices and a large common offset does not cancel.
+// elements, and (count, mean, M2) are merged by Chan's update, so a large
+// common offset does not cancel.
 //
 // dw and db: every CTA keeps the column sums of its rows in registers (its
 // thread groups added in order at the end) and writes one fp32 partial row;
@@ -170,6 +175,461 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT) layer_norm_kernel(
   }
 }
 
+// ---- rows of 16-byte pieces, one thread per piece -------------------------------------
+// PIECES 16-byte pieces a thread, S rows in the ring (S - 1 of them in flight).
+// A thread reads back only what it copied itself: no barrier guards the ring.
+__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Two fp32 values in one 64-bit register: the packed instructions (each half
+// rounded as its scalar form) halve the instructions issued per element, which
+// bound these kernels before HBM did.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float both(f32x2 v) {
+  const float2 f = split2(v);
+  return f.x + f.y;
+}
+
+// A 16-byte piece of a row as pairs.
+template <typename T>
+struct Pack {
+  static constexpr int N = 16 / sizeof(T), P = N / 2;
+};
+__device__ __forceinline__ void unpack(const uint4& u, f32x2 (&v)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pair2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const uint4& u, f32x2 (&v)[2], float) {
+  v[0] = pair2(__uint_as_float(u.x), __uint_as_float(u.y));
+  v[1] = pair2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 pack(const f32x2 (&v)[4], __nv_bfloat16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = split2(v[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const f32x2 (&v)[2], float) {
+  const float2 a = split2(v[0]), b = split2(v[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                    __float_as_uint(b.y));
+}
+template <int P>
+__device__ __forceinline__ void load_f32(const float* p, f32x2 (&v)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; i += 2) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p + 2 * i));
+    v[i] = pair2(f.x, f.y);
+    v[i + 1] = pair2(f.z, f.w);
+  }
+}
+
+// Sums over a warp of N values (1, 2 or 4) at once: every exchange halves the
+// values a lane carries, so 4 values take 6 exchanges instead of 20.  Lane l
+// ends with the total of value slot(l) = l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2, o /= 2) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[n / 2 + i] : v[i], give = up ? v[i] : v[n / 2 + i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (; o > 0; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+// Block-wide sums of N values, given each warp's in buf[value][warp]: value i
+// to every lane.  Two warps' values a lane and 32 / N lanes a value.
+template <int N>
+__device__ __forceinline__ void block_sums(const float (*buf)[32], int warps, float (&out)[N]) {
+  constexpr int L = 32 / N;
+  const int lane = threadIdx.x & 31, w = lane % L;
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (w + i * L < warps) r += buf[lane / L][w + i * L];
+#pragma unroll
+  for (int o = L / 2; o > 0; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = __shfl_sync(0xffffffffu, r, i * L);
+}
+
+// A CTA's rows blockIdx.x, blockIdx.x + gridDim.x, .. on their way through the
+// ring: OPS operands of PIECES pieces a thread.  Addresses advance by constants.
+template <typename T, int OPS, int PIECES, int ROWS, int S>
+struct Ring {
+  const uint4* mem;
+  const char* src[OPS];    // this thread's first piece of the next row to fetch
+  size_t row_step;         // bytes from one of the CTA's rows to the next
+  uint32_t base, row_bytes, piece_bytes;  // shared memory
+  uint32_t put, get;       // byte offsets of the slots fetched and read next
+  int left;                // rows to fetch
+  bool in[PIECES];         // this thread's piece i exists
+  __device__ __forceinline__ Ring(const uint4* ring, int rows, int d) {
+    const int kT = blockDim.x, t = threadIdx.x;
+    mem = ring;
+    piece_bytes = (uint32_t)kT * 16;
+    row_bytes = OPS * PIECES * piece_bytes;
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (uint32_t)t * 16;
+    row_step = (size_t)gridDim.x * d * sizeof(T);
+    put = get = 0;
+    left = rows;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) in[i] = (i * kT + t) * (int)(16 / sizeof(T)) < d;
+  }
+  __device__ __forceinline__ void operand(int op, const T* p, int d) {
+    src[op] = reinterpret_cast<const char*>(p + (size_t)blockIdx.x * d) + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ void fetch() {  // the next ROWS rows, one group
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k, --left) {
+      if (left > 0) {
+#pragma unroll
+        for (int op = 0; op < OPS; ++op) {
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i)
+            if (in[i])
+              copy16(base + put + k * row_bytes + (op * PIECES + i) * piece_bytes,
+                     src[op] + i * piece_bytes);
+          src[op] += row_step;
+        }
+      }
+    }
+    copy_commit();
+    put = put == (S - ROWS) * row_bytes ? 0 : put + ROWS * row_bytes;
+  }
+  __device__ __forceinline__ uint4 read(int k, int op, int i) const {
+    return mem[(get + k * row_bytes + (op * PIECES + i) * piece_bytes) / 16 + threadIdx.x];
+  }
+  __device__ __forceinline__ void next() {
+    get = get == (S - ROWS) * row_bytes ? 0 : get + ROWS * row_bytes;
+  }
+};
+
+// ROWS rows at a time: their reductions overlap, and a reduction's instructions
+// are shared by 16 elements a thread.  8192 x 7168 bf16: forward 54 us (4.3
+// TB/s, 0.66 of the measured copy), backward 101 us with the column sums (3.5
+// TB/s); what is left is instruction issue and the wait for a row's reduction.
+// Measured and not taken: 8 elements a thread and one row at a time, a CTA of
+// 896 threads (72 and 116 us); one row at a time in two CTAs an SM (57 and
+// 100 us).
+template <typename T, int PIECES, int ROWS, int S>
+__global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
+    const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, float eps,
+    int R, int d, T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+  static_assert(S % ROWS == 0 && S > ROWS, "whole iterations in the ring");
+  constexpr int V = Pack<T>::N, P = Pack<T>::P;
+  extern __shared__ uint4 ring[];        // [S][PIECES][kT]
+  __shared__ float part[2][ROWS][3][32];   // count, mean, M2 of each warp
+  const int kT = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, warps = kT >> 5;
+  const long long step = gridDim.x;
+  auto fetch = [&](long long r, int slot) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+      if (r + k * step < R) {
+        const T* src = x + (size_t)(r + k * step) * d;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int c = (i * kT + t) * V;
+          if (c < d) copy16(static_cast<uint32_t>(__cvta_generic_to_shared(
+                           &ring[((slot + k) * PIECES + i) * kT + t])),
+                       src + c);
+        }
+      }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - ROWS; i += ROWS) fetch(blockIdx.x + i * step, i);
+  f32x2 wv[PIECES][P], bv[PIECES][P];  // this thread's columns never change
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = (i * kT + t) * V;
+#pragma unroll
+    for (int e = 0; e < P; ++e) wv[i][e] = bv[i][e] = 0ull;
+    if (c < d) {
+      load_f32(w + c, wv[i]);
+      if (b != nullptr) load_f32(b + c, bv[i]);
+    }
+  }
+  const float inv_d = 1.f / (float)d;
+  // all lanes of the warp hold PIECES whole pieces
+  const bool whole = ((PIECES - 1) * kT + (warp + 1) * 32) * V <= d;
+  int slot = 0, flip = 0;
+  for (long long r = blockIdx.x; r < R; r += ROWS * step, flip ^= 1) {
+    fetch(r + (S - ROWS) * step, slot == 0 ? S - ROWS : slot - ROWS);
+    copy_wait<S / ROWS - 1>();
+    f32x2 v[ROWS][PIECES][P];
+    Stat s[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      s[k] = Stat{0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if ((i * kT + t) * V < d) {
+          unpack(ring[((slot + k) * PIECES + i) * kT + t], v[k][i], T{});
+          f32x2 sum = v[k][i][0];
+#pragma unroll
+          for (int e = 1; e < P; ++e) sum = add2(sum, v[k][i][e]);
+          const float m = both(sum) * (1.f / V);
+          const f32x2 m1 = pair2(-m, -m);
+          f32x2 sq = 0ull;
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f32x2 c = add2(v[k][i][e], m1);
+            sq = fma2(c, c, sq);
+          }
+          const float m2 = both(sq);
+          if (i == 0) {
+            s[k] = Stat{(float)V, m, m2};
+          } else {  // equal counts so far: i pieces and one more
+            const float dm = m - s[k].mean;
+            s[k].mean = fmaf(dm, 1.f / (i + 1), s[k].mean);
+            s[k].m2 = fmaf(dm * dm, V * (float)i / (i + 1), s[k].m2 + m2);
+            s[k].n += V;
+          }
+        }
+    }
+    slot = slot == S - ROWS ? 0 : slot + ROWS;
+    if (whole) {  // equal counts: the merged mean is the middle of the two
+      float n = PIECES * V;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1, n *= 2.f)
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          const float m = __shfl_xor_sync(0xffffffffu, s[k].mean, o);
+          const float m2 = __shfl_xor_sync(0xffffffffu, s[k].m2, o);
+          const float dm = m - s[k].mean;
+          s[k].mean = 0.5f * (s[k].mean + m);
+          s[k].m2 = fmaf(dm * dm, 0.5f * n, s[k].m2 + m2);
+          s[k].n = 2.f * n;
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) s[k] = warp_merge(s[k]);
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        part[flip][k][0][warp] = s[k].n;
+        part[flip][k][1][warp] = s[k].mean;
+        part[flip][k][2][warp] = s[k].m2;
+      }
+    __syncthreads();
+    // the warps' statistics: mean first, then the squares around it.  Lanes
+    // 0-15 take the first row, lanes 16-31 the second (ROWS == 1: all lanes)
+    constexpr int L = 32 / ROWS;
+    const int k0 = lane / L, w0 = lane % L;
+    float cn[ROWS], cm[ROWS], cs[ROWS], a = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int q = w0 + i * L;
+      const bool in = q < warps;
+      cn[i] = in ? part[flip][k0][0][q] : 0.f;
+      cm[i] = in ? part[flip][k0][1][q] : 0.f;
+      cs[i] = in ? part[flip][k0][2][q] : 0.f;
+      a = fmaf(cn[i], cm[i], a);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float mk = a * inv_d;
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const float dm = cm[i] - mk;
+      a += fmaf(cn[i] * dm, dm, cs[i]);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float rk1 = rsqrtf(a * inv_d + eps);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const long long rk = r + k * step;
+      if (rk >= R) break;
+      const float mu = __shfl_sync(0xffffffffu, mk, k * L), rs = __shfl_sync(0xffffffffu, rk1, k * L);
+      if (t == 0) {
+        mean[rk] = mu;
+        rstd[rk] = rs;
+      }
+      const f32x2 mu2 = pair2(-mu, -mu), rs2 = pair2(rs, rs);
+      T* dst = y + (size_t)rk * d;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int c = (i * kT + t) * V;
+        if (c < d) {
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            v[k][i][e] = fma2(mul2(add2(v[k][i][e], mu2), rs2), wv[i][e], bv[i][e]);
+          *reinterpret_cast<uint4*>(dst + c) = pack(v[k][i], T{});
+        }
+      }
+    }
+  }
+  copy_wait<0>();
+}
+
+// One partial row of dw and db per CTA, as below.
+template <typename T, int PIECES, int ROWS, int S>
+__global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
+    const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ mean, const float* __restrict__ rstd, int R, int d,
+    T* __restrict__ dx, float* __restrict__ part) {
+  static_assert(S % ROWS == 0 && S > ROWS, "whole iterations in the ring");
+  constexpr int V = Pack<T>::N, P = Pack<T>::P;
+  extern __shared__ uint4 ring[];  // [S][2][PIECES][kT]
+  __shared__ float red[2][2 * ROWS][32];
+  const int kT = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, warps = kT >> 5;
+  const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's
+  Ring<T, 2, PIECES, ROWS, S> in(ring, rows, d);
+  in.operand(0, x, d);
+  in.operand(1, dy, d);
+#pragma unroll
+  for (int i = 0; i < S - ROWS; i += ROWS) in.fetch();
+  f32x2 wv[PIECES][P], aw[PIECES][P], ab[PIECES][P];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = (i * kT + t) * V;
+#pragma unroll
+    for (int e = 0; e < P; ++e) wv[i][e] = aw[i][e] = ab[i][e] = 0ull;
+    if (c < d) load_f32(w + c, wv[i]);
+  }
+  const float inv_d = 1.f / (float)d;
+  float mu[ROWS], rs[ROWS];
+  const float* mp = mean + blockIdx.x;
+  const float* rp = rstd + blockIdx.x;
+  auto row_stats = [&](int at, float (&m)[ROWS], float (&q)[ROWS]) {  // rows at, at + 1, ..
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      m[k] = q[k] = 0.f;
+      if (at + k < rows) {
+        m[k] = __ldg(mp);
+        q[k] = __ldg(rp);
+        mp += gridDim.x;
+        rp += gridDim.x;
+      }
+    }
+  };
+  row_stats(0, mu, rs);
+  char* dst = reinterpret_cast<char*>(dx + (size_t)blockIdx.x * d) + t * 16;
+  int flip = 0;
+  for (int done = 0; done < rows; done += ROWS, flip ^= 1) {
+    in.fetch();
+    float mu1[ROWS], rs1[ROWS];  // the next rows'
+    row_stats(done + ROWS, mu1, rs1);
+    copy_wait<S / ROWS - 1>();
+    f32x2 z[ROWS][PIECES][P], h[ROWS][PIECES][P];
+    float sums[2 * ROWS];  // h of each row, then h z of each row
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      f32x2 s1 = 0ull, s2 = 0ull;
+      if (done + k < rows) {
+        const f32x2 mu2 = pair2(-mu[k], -mu[k]), rs2 = pair2(rs[k], rs[k]);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+          if (in.in[i]) {
+            f32x2 g[P];
+            unpack(in.read(k, 0, i), z[k][i], T{});
+            unpack(in.read(k, 1, i), g, T{});
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              z[k][i][e] = mul2(add2(z[k][i][e], mu2), rs2);
+              h[k][i][e] = mul2(g[e], wv[i][e]);
+              s1 = add2(s1, h[k][i][e]);
+              s2 = fma2(h[k][i][e], z[k][i][e], s2);
+              aw[i][e] = fma2(g[e], z[k][i][e], aw[i][e]);
+              ab[i][e] = add2(ab[i][e], g[e]);
+            }
+          }
+      }
+      sums[k] = both(s1);
+      sums[ROWS + k] = both(s2);
+    }
+    in.next();
+    const float mine = warp_sums<2 * ROWS>(sums);
+    if (lane % (16 / ROWS) == 0) red[flip][lane / (16 / ROWS)][warp] = mine;
+    __syncthreads();
+    block_sums<2 * ROWS>(red[flip], warps, sums);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      if (done + k >= rows) break;
+      // dx = rs h - rs (mean(h) + z mean(h z))
+      const float a = -rs[k] * (sums[k] * inv_d), c = -rs[k] * (sums[ROWS + k] * inv_d);
+      const f32x2 rs2 = pair2(rs[k], rs[k]), a2 = pair2(a, a), c2 = pair2(c, c);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if (in.in[i]) {
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            z[k][i][e] = fma2(h[k][i][e], rs2, fma2(z[k][i][e], c2, a2));
+          *reinterpret_cast<uint4*>(dst + i * in.piece_bytes) = pack(z[k][i], T{});
+        }
+      dst += in.row_step;
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      mu[k] = mu1[k];
+      rs[k] = rs1[k];
+    }
+  }
+  copy_wait<0>();
+  float* prow = part + (size_t)blockIdx.x * 2 * d;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = (i * kT + t) * V;
+    if (c < d) {
+#pragma unroll
+      for (int e = 0; e < P; e += 2) {
+        *reinterpret_cast<ulonglong2*>(prow + c + 2 * e) = make_ulonglong2(aw[i][e], aw[i][e + 1]);
+        *reinterpret_cast<ulonglong2*>(prow + d + c + 2 * e) =
+            make_ulonglong2(ab[i][e], ab[i][e + 1]);
+      }
+    }
+  }
+}
+
+// ---- elements in registers --------------------------------------------------------------
 // One partial row of dw and db per CTA: part [gridDim.x][2][d].
 template <typename T, int VEC, int PIECES, int kT>
 __global__ void __launch_bounds__(kT < 128 ? 128 : kT) layer_norm_bwd_kernel(
@@ -298,34 +758,64 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT) layer_norm_bwd_kernel(
   }
 }
 
-// out[c] = sum over the P partial rows, in a fixed order: 8 chains of rows
-// p, p + 8, .. per column, added in chain order.
+// out[c] = sum over the P partial rows, in a fixed order: 32 chains of rows p,
+// p + 32, .. per column, then the chains.  A thread owns 4 columns (1 where d is
+// odd) of its chain.  Launched to overlap the end of the kernel before it.
+template <int V>
 __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int P,
                                                           int d, float* __restrict__ dw,
                                                           float* __restrict__ db) {
-  __shared__ float s[8][33];
-  const int cx = threadIdx.x & 31, cy = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cx;
-  float v = 0.f;
-  if (c < 2 * d)
-    for (int p = cy; p < P; p += 8) v += part[(size_t)p * 2 * d + c];
-  s[cy][cx] = v;
-  __syncthreads();
-  if (cy == 0 && c < 2 * d) {
+  __shared__ float s[32][8 * V + 1];
+  const int cx = threadIdx.x & 7, cy = threadIdx.x >> 3;
+  const int c = (blockIdx.x * 8 + cx) * V;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float v[V] = {};
+  if (c < 2 * d) {
+#pragma unroll 4
+    for (int p = cy; p < P; p += 32) {
+      const float* src = part + (size_t)p * 2 * d + c;
+      if constexpr (V == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[0] += f.x;
+        v[1] += f.y;
+        v[2] += f.z;
+        v[3] += f.w;
+      } else {
+        v[0] += *src;
+      }
+    }
+  }
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][cx];
-    if (c < d)
-      dw[c] = v;
+  for (int e = 0; e < V; ++e) s[cy][cx * V + e] = v[e];
+  __syncthreads();
+  const int t = threadIdx.x, out = blockIdx.x * 8 * V + t;
+  if (t < 8 * V && out < 2 * d) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[i][t];
+    if (out < d)
+      dw[out] = sum;
     else if (db != nullptr)
-      db[c - d] = v;
+      db[out - d] = sum;
   }
 }
 
-// CTAs of the backward kernel = partial rows: at most two per SM.
-int bwd_ctas(int R, int d) {
+// The row kernels take rows of whole 16-byte pieces, wider than a warp's, two
+// pieces a thread.  Up to 16 KB a row: two rows at a time, a ring of six; up to
+// 32 KB: one at a time, a ring of three (what fits in shared memory).
+bool by_rows(int d, int elem) { return d > 1024 && d % (16 / elem) == 0 && d * elem <= 32768; }
+int row_threads(int d, int elem) { return ((d / (16 / elem) + 1) / 2 + 31) / 32 * 32; }
+int rows_per_sm(int d, int elem) {  // CTAs of a row kernel on an SM: 512 threads in all
+  const int t = row_threads(d, elem);
+  return t >= 512 ? 1 : 512 / t;
+}
+// CTAs of the backward kernel = partial rows.
+int bwd_ctas(int R, int d, int elem) {
+  const bool rows = by_rows(d, elem);
   const int groups = d <= 1024 ? 4 : 1;
   const long long want = ((long long)R + groups - 1) / groups;
-  return (int)(want < 2 * 148 ? (want < 1 ? 1 : want) : 2 * 148);
+  const long long most = 148LL * (rows ? rows_per_sm(d, elem) : 2);
+  return (int)(want < most ? (want < 1 ? 1 : want) : most);
 }
 
 struct Fwd {
@@ -356,9 +846,42 @@ template <typename T, int VEC, int PIECES, int kT>
 void go(const Bwd& a, cudaStream_t st) {
   constexpr int kBlock = kT < 128 ? 128 : kT;
   const size_t smem = kBlock > kT ? (size_t)2 * a.d * 4 : 0;
-  layer_norm_bwd_kernel<T, VEC, PIECES, kT><<<bwd_ctas(a.R, a.d), kBlock, smem, st>>>(
+  layer_norm_bwd_kernel<T, VEC, PIECES, kT><<<bwd_ctas(a.R, a.d, sizeof(T)), kBlock, smem, st>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.mean, a.rstd, a.R, a.d,
       static_cast<T*>(a.dx), a.part);
+}
+
+template <typename T, int ROWS, int S>
+cudaError_t rows_launch(const Fwd& a, cudaStream_t st) {
+  const int kT = row_threads(a.d, sizeof(T));
+  const size_t smem = (size_t)S * 2 * kT * 16;
+  auto kernel = row_kernel<T, 2, ROWS, S>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  const int most = 148 * rows_per_sm(a.d, sizeof(T));
+  kernel<<<a.R < most ? a.R : most, kT, smem, st>>>(static_cast<const T*>(a.x), a.w, a.b, a.eps,
+                                                    a.R, a.d, static_cast<T*>(a.y), a.mean,
+                                                    a.rstd);
+  return cudaGetLastError();
+}
+template <typename T, int ROWS, int S>
+cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
+  const int kT = row_threads(a.d, sizeof(T));
+  const size_t smem = (size_t)S * 2 * 2 * kT * 16;
+  auto kernel = row_bwd_kernel<T, 2, ROWS, S>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<bwd_ctas(a.R, a.d, sizeof(T)), kT, smem, st>>>(
+      static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.mean, a.rstd, a.R, a.d,
+      static_cast<T*>(a.dx), a.part);
+  return cudaGetLastError();
+}
+template <typename T, typename Args>
+cudaError_t rows(const Args& a, cudaStream_t st) {
+  if (a.d * (int)sizeof(T) <= 16384) return rows_launch<T, 2, 6>(a, st);
+  return rows_launch<T, 1, 3>(a, st);
 }
 
 // Threads per row and elements per thread by width: as few threads as hold the
@@ -374,7 +897,9 @@ void by_width(const Args& a, cudaStream_t st) {
   else go<T, VEC, 32 / VEC, 512>(a, st);
 }
 template <typename Args>
-void by_type(const Args& a, int dtype, cudaStream_t st) {
+cudaError_t by_type(const Args& a, int dtype, cudaStream_t st) {
+  if (by_rows(a.d, (int)dtype_bytes(dtype)))
+    return dtype == MOE_DTYPE_BF16 ? rows<__nv_bfloat16>(a, st) : rows<float>(a, st);
   if (dtype == MOE_DTYPE_BF16) {
     if (a.d % 8 == 0) by_width<__nv_bfloat16, 8>(a, st);
     else by_width<__nv_bfloat16, 1>(a, st);
@@ -382,18 +907,22 @@ void by_type(const Args& a, int dtype, cudaStream_t st) {
     if (a.d % 4 == 0) by_width<float, 4>(a, st);
     else by_width<float, 1>(a, st);
   }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 int layer_norm_max_d() { return kMaxD; }
 
-size_t layer_norm_ws_bytes(int R, int d) { return (size_t)bwd_ctas(R, d) * 2 * d * 4; }
+size_t layer_norm_ws_bytes(int R, int d) {  // for either type
+  const int a = bwd_ctas(R, d, 2), b = bwd_ctas(R, d, 4);
+  return (size_t)(a > b ? a : b) * 2 * d * 4;
+}
 
 cudaError_t launch_layer_norm(int dtype, const void* x, const float* w, const float* b, float eps,
                               int R, int d, void* y, float* mean, float* rstd, cudaStream_t st) {
-  by_type(Fwd{x, w, b, eps, R, d, y, mean, rstd}, dtype, st);
-  return note_cuda(cudaGetLastError(), "layer norm launch");
+  return note_cuda(by_type(Fwd{x, w, b, eps, R, d, y, mean, rstd}, dtype, st),
+                   "layer norm launch");
 }
 
 cudaError_t launch_layer_norm_backward(int dtype, const void* dy, const void* x, const float* w,
@@ -401,11 +930,22 @@ cudaError_t launch_layer_norm_backward(int dtype, const void* dy, const void* x,
                                        void* dx, float* dw, float* db, void* ws,
                                        cudaStream_t st) {
   float* part = static_cast<float*>(ws);
-  by_type(Bwd{dy, x, w, mean, rstd, R, d, dx, part}, dtype, st);
-  cudaError_t e = note_cuda(cudaGetLastError(), "layer norm backward launch");
+  cudaError_t e = note_cuda(by_type(Bwd{dy, x, w, mean, rstd, R, d, dx, part}, dtype, st),
+                            "layer norm backward launch");
   if (e != cudaSuccess) return e;
-  column_sums_kernel<<<(2 * d + 31) / 32, 256, 0, st>>>(part, bwd_ctas(R, d), d, dw, db);
-  return note_cuda(cudaGetLastError(), "layer norm column sums launch");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int P = bwd_ctas(R, d, (int)dtype_bytes(dtype)), v = d % 4 == 0 ? 4 : 1;
+  cfg.gridDim = dim3((unsigned)((2 * d + 8 * v - 1) / (8 * v)), 1, 1);
+  return note_cuda(cudaLaunchKernelEx(&cfg, v == 4 ? column_sums_kernel<4> : column_sums_kernel<1>,
+                                      (const float*)part, P, d, dw, db),
+                   "layer norm column sums launch");
 }
 
 }  // namespace moe

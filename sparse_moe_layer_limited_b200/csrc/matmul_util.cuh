@@ -16,12 +16,31 @@ constexpr uint64_t kMatmulTimeoutNs = 2000000000ull;
 // good groups; and the clock is first read after 64 tries, as reading it on
 // every wait that does not succeed at once delays the pipeline.  kCluster:
 // cluster-scope acquire, for barriers the peer CTA arrives on.
+__device__ __forceinline__ bool mm_try(uint64_t* bar, uint32_t parity, bool cluster) {
+  constexpr uint32_t kSuspendNs = 20000;  // the warp sleeps up to this long per try
+  uint32_t ok;
+  if (cluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+  return ok != 0;
+}
 template <bool kCluster = false>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                         uint64_t limit_ns = kMatmulTimeoutNs) {
-  auto ready = [&] {
-    return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  };
+  auto ready = [&] { return mm_try(bar, parity, kCluster); };
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (ready()) return true;
