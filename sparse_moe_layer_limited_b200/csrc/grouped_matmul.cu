@@ -42,11 +42,10 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "epilogue.cuh"
 #include "internal.h"
 #include "matmul_util.cuh"
+#include "pair_launch.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
         for (int j = 0; j < t.tiles && ok; ++j) {
           const uint32_t ap = (((use + j) >> 1) & 1) ^ 1u;
           ok = mm_wait(&edone[(use + j) & 1], ap, args.status) &&
-               mm_wait<true>(&tempty[(use + j) & 1], ap, args.status);
+               mm_wait(&tempty[(use + j) & 1], ap, args.status);
         }
         if (!ok) break;
         tc_fence_after();
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
         const Unit t = decode(u);
         for (int j = 0; j < t.tiles && ok; ++j, ++use) {
           ok = mm_wait(&edone[use & 1], (use >> 1) & 1, args.status);
-          if (ok) mbar_arrive_cluster(tempty0 + 8u * (uint32_t)(use & 1));
+          if (ok) mbar_arrive_peer(tempty0 + 8u * (uint32_t)(use & 1));
         }
       }
     }
@@ -546,36 +545,9 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
 
 template <int kMode, int kShare>
 cudaError_t launch_pair(const GArgs& a, long long units, cudaStream_t st) {
-  auto kernel = grouped_matmul_pair_kernel<kMode, kShare>;
-  const size_t smem = pair_smem(kMode, kShare, a.E);
-  cudaError_t e =
-      note_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)pair_smem(kMode, kShare, kMatmulMaxGroups)),
-                "grouped matmul: set shared-memory size");
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(pair_threads(kMode), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(num_sms() & ~1), 1, 1);
-  // as many pairs as can be resident at once (one CTA per SM whatever E is)
-  static std::atomic<int> resident{0};
-  int pairs = resident.load();
-  if (pairs == 0) {
-    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0)
-      pairs = num_sms() / 2;
-    resident.store(pairs);
-  }
-  if (units < pairs) pairs = (int)units;
-  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-  return note_cuda(cudaLaunchKernelEx(&cfg, kernel, a), "grouped matmul launch");
+  return launch_pairs(grouped_matmul_pair_kernel<kMode, kShare>, a, pair_smem(kMode, kShare, a.E),
+                      pair_smem(kMode, kShare, kMode == kDw ? 0 : kMatmulMaxGroups),
+                      pair_threads(kMode), units, "grouped matmul", st);
 }
 
 }  // namespace

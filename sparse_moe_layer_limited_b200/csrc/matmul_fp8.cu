@@ -7,11 +7,17 @@
 // forward: its weight operand has the contraction index outermost.
 //
 // Each 128-wide slice of a 128 x 256 output tile is one product on the tensor
-// cores (fp32, exact per-slice sums of the codes' products up to fp32
-// accumulation) into one of two 256-column TMEM buffers; eight epilogue warps
+// cores (fp32) into one of two 256-column TMEM buffers; eight epilogue warps
 // multiply it by the two scales and add it to fp32 registers, 128 running sums
 // a thread, while the next slice fills the other buffer.  The scales are read
-// from global memory four slices ahead.  The result is rounded once to bf16.
+// from global memory two slices ahead.  The result is rounded once to bf16.
+//
+// 8192 x 4096 x 7168: 245 us at 1.8 GHz (1.96 PFLOP/s), 286 us under sustained
+// power.  Of a slice's 1100 cycles 512 are MMA; without the promotion's reads
+// of TMEM the kernel takes 197 us, with half the operand traffic as well 170
+// us, without the multiply-adds no less than with them.  Measured and not
+// taken: CTA pairs (a third less operand traffic: 240 us dense, but 256-row
+// tiles cost ragged experts 25%).
 //
 // Also here: the quantisers that make the codes, per 1x128 tile of a row and
 // per 128x128 block (tile_scale below).
@@ -33,10 +39,10 @@ constexpr int PStages = 4;
 constexpr int PABytes = PBM * PBK;
 constexpr int PStageBytes = PABytes + PBN * PBK;
 constexpr int PEpiWarps = 8;
-constexpr int PThreads = 64 + 32 * PEpiWarps;
+constexpr int PThreads = 128 + 32 * PEpiWarps;  // a warpgroup of control warps, two of epilogue
 constexpr int PStg = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 constexpr int PCols = PBN / 2;  // columns per epilogue warp
-constexpr int kAhead = 4;       // slices whose scales are loaded together
+constexpr int kAhead = 2;       // slices whose scales are loaded together
 
 constexpr size_t fp8_mm_smem(int E) {
   return 1024 + (size_t)PStages * PStageBytes + PEpiWarps * PStg + 256 + (size_t)(E + 1) * 4;
@@ -46,7 +52,8 @@ static_assert(fp8_mm_smem(kMatmulMaxGroups) <= 232448, "shared-memory opt-in");
 struct alignas(64) PArgs {
   CUtensorMap tmA;    // row codes [R, K], box {128, 128}
   CUtensorMap tmA32;  // the same, box {128, 32}
-  CUtensorMap tmB;    // weight codes [E, n, k]: fwd box {128, 64, 1}, dx box {128, 128, 1}
+  CUtensorMap tmB;    // weight codes [E, n, k]: fwd box {128, 256, 1}, dx box {128, 128, 1}
+  CUtensorMap tmB64;  // fwd: box {128, 64, 1}, for a narrow last column tile
   CUtensorMap tmOut;  // out [R, cols] bf16, box {64, 32} (cols % 8 == 0)
   const int32_t* offsets;
   const float* sa;  // [KB, sa_ld]
@@ -85,7 +92,8 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int NT = (args.cols + PBN - 1) / PBN;
   const int KB = (args.kdim + PBK - 1) / PBK;
 
@@ -127,93 +135,124 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
     return t;
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&args.tmA);
-      tma_prefetch_desc(&args.tmB);
+  // 384 threads launch with 168 registers each; the control warps hand 96 of
+  // theirs to the epilogue: 128 * 72 + 256 * 216 = 384 * 168
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ---- TMA producer: the warp walks the loop together, so that addresses stay
+      // warp-uniform, and one lane issues ----
+      if (elect_one()) {
+        tma_prefetch_desc(&args.tmA);
+        tma_prefetch_desc(&args.tmB);
+      }
+      __syncwarp();
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
+      Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit t = decode(u);
-        const int nc =
-            min(PBN / kChunkCols, (args.cols - t.n * PBN + kChunkCols - 1) / kChunkCols);
+        Unit next = t;
+        const int nc = min(PBN / kChunkCols, (args.cols - t.n * PBN + kChunkCols - 1) / kChunkCols);
         const int na = min(4, (t.rows - t.m * PBM + 31) / 32);
         const int r = t.first + t.m * PBM;
         const uint32_t bytes = (uint32_t)(nc * kChunk + na * 32 * PBK);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mm_wait(&empty[stage], phase ^ 1u, args.status)) {
-            ok = false;
-            break;
-          }
+          ok = mm_wait(&empty[stage], phase ^ 1u, args.status);
+          if (!ok) break;
           uint8_t* sa = base + (size_t)stage * PStageBytes;
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          if (na == 4) {
-            tma_load_2d(sa, &args.tmA, kb * PBK, r, &full[stage]);
-          } else {
-            for (int c = 0; c < na; ++c)
-              tma_load_2d(sa + c * (32 * PBK), &args.tmA32, kb * PBK, r + 32 * c, &full[stage]);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            if (na == 4) {
+              tma_load_2d(sa, &args.tmA, kb * PBK, r, &full[stage]);
+            } else {
+              for (int c = 0; c < na; ++c)
+                tma_load_2d(sa + c * (32 * PBK), &args.tmA32, kb * PBK, r + 32 * c, &full[stage]);
+            }
+            if (nc == PBN / kChunkCols && kDx == 0) {
+              tma_load_3d(sa + PABytes, &args.tmB, kb * PBK, t.n * PBN, t.g, &full[stage]);
+            } else {
+              for (int c = 0; c < nc; ++c) {
+                const int col = t.n * PBN + kChunkCols * c;
+                if constexpr (kDx)
+                  tma_load_3d(sa + PABytes + c * kChunk, &args.tmB, col, kb * PBK, t.g,
+                              &full[stage]);
+                else
+                  tma_load_3d(sa + PABytes + c * kChunk, &args.tmB64, kb * PBK, col, t.g,
+                              &full[stage]);
+              }
+            }
           }
-          for (int c = 0; c < nc; ++c) {
-            const int col = t.n * PBN + kChunkCols * c;
-            if constexpr (kDx)
-              tma_load_3d(sa + PABytes + c * kChunk, &args.tmB, col, kb * PBK, t.g, &full[stage]);
-            else
-              tma_load_3d(sa + PABytes + c * kChunk, &args.tmB, kb * PBK, col, t.g, &full[stage]);
-          }
+          __syncwarp();
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == PStages) {
             stage = 0;
             phase ^= 1u;
           }
+          // the next unit is looked up while this one's copies are in flight
+          if (kb == 0 && u + (int)gridDim.x < total) next = decode(u + gridDim.x);
         }
+        t = next;
       }
       if (!ok) {
         for (int s = 0; s < PStages; ++s)
           if ((issued >> s) & 1u)
             mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1) {
+      // ---- MMA issuer, one TMEM buffer per slice ----
+      const uint32_t ring = smem_u32(base);
+      const uint64_t ad0 = smem_desc_sw128(ring);
+      const uint64_t bd0 = kDx ? smem_desc_mn_sw128(ring + PABytes, kChunk)
+                               : smem_desc_sw128(ring + PABytes);
+      const uint32_t a_hi = desc_hi(ad0), b_hi = desc_hi(bd0);
+      constexpr uint32_t kBStep = (kDx ? 4096 : 32) / 16;
       int stage = 0;
       uint32_t phase = 0, slice = 0;
       bool ok = true;
+      Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit t = decode(u);
+        Unit next = t;
         const int width = min(PBN, args.cols - t.n * PBN);
         const uint32_t idesc = idesc_f8_f32(PBM, (width + 15) / 16 * 16, args.a_fmt, kF8E4M3) |
                                (kDx ? kIdescBMn : 0u);
         for (int kb = 0; kb < KB; ++kb, ++slice) {
           const uint32_t sb = slice & 1u;
-          if (!mm_wait(&sempty[sb], ((slice >> 1) & 1u) ^ 1u, args.status) ||
-              !mm_wait(&full[stage], phase, args.status)) {
-            ok = false;
-            break;
-          }
+          ok = mm_wait(&sempty[sb], ((slice >> 1) & 1u) ^ 1u, args.status) &&
+               mm_wait(&full[stage], phase, args.status);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(base + (size_t)stage * PStageBytes), b0 = a0 + PABytes;
-#pragma unroll
-          for (int k = 0; k < PBK / 32; ++k)
-            mma_e4m3(tmem_base + sb * PBN, smem_desc_sw128(a0 + k * 32),
-                     kDx ? smem_desc_mn_sw128(b0 + k * 4096, kChunk) : smem_desc_sw128(b0 + k * 32),
-                     idesc, k != 0);
-          mma_commit(&empty[stage]);
-          mma_commit(&sfull[sb]);
+          const uint32_t off = (uint32_t)stage * (PStageBytes / 16);
+          const uint32_t a_lo = desc_lo(ad0) + off, b_lo = desc_lo(bd0) + off;
+          if (elect_one()) {
+  #pragma unroll
+            for (int k = 0; k < PBK / 32; ++k)
+              mma_f8_parts(tmem_base + sb * PBN, a_lo + k * 2, a_hi, b_lo + k * kBStep, b_hi, idesc,
+                           k != 0);
+            mma_commit(&empty[stage]);
+            mma_commit(&sfull[sb]);
+          }
+          __syncwarp();
           if (++stage == PStages) {
             stage = 0;
             phase ^= 1u;
           }
+          if (kb == 0 && u + (int)gridDim.x < total) next = decode(u + gridDim.x);
         }
+        t = next;
       }
-      mma_commit(drain);
-      mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
+      if (elect_one()) {
+        mma_commit(drain);
+        mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
+      }
+      __syncwarp();
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- promotion and epilogue: two warps per lane quadrant, 128 columns each ----
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stg = staging + (size_t)(warp - 2) * PStg;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* stg = staging + (size_t)(warp - 4) * PStg;
     const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + half * PCols;
     const bool tma_out = (args.cols & 7) == 0;
     uint32_t slice = 0;
@@ -232,24 +271,30 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
       float acc[PCols];
 #pragma unroll
       for (int i = 0; i < PCols; ++i) acc[i] = 0.f;
-      float cur[kAhead], nxt[kAhead];
-      auto scales = [&](float (&s)[kAhead], int kb) {
+      // loaded kAhead slices ahead, multiplied when used
+      float row_sc[kAhead], w_sc[kAhead], row_nx[kAhead], w_nx[kAhead];
+      auto scales = [&](float (&r)[kAhead], float (&q)[kAhead], int kb) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          s[j] = 0.f;
-          if (live && kb + j < KB)
-            s[j] = __ldg(sa + (size_t)(kb + j) * args.sa_ld) *
-                   __ldg(sw + (size_t)(kb + j) * sw_step);
+          r[j] = q[j] = 0.f;
+          if (live && kb + j < KB) {
+            r[j] = __ldg(sa + (size_t)(kb + j) * args.sa_ld);
+            q[j] = __ldg(sw + (size_t)(kb + j) * sw_step);
+          }
         }
       };
-      scales(nxt, 0);
+      scales(row_nx, w_nx, 0);
       for (int kb = 0; kb < KB && ok; kb += kAhead) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) cur[j] = nxt[j];
-        scales(nxt, kb + kAhead);
+        for (int j = 0; j < kAhead; ++j) {
+          row_sc[j] = row_nx[j];
+          w_sc[j] = w_nx[j];
+        }
+        scales(row_nx, w_nx, kb + kAhead);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           if (kb + j >= KB) break;
+          const float sc = row_sc[j] * w_sc[j];
           const uint32_t sb = slice & 1u;
           if (!mm_wait(&sfull[sb], (slice >> 1) & 1u, args.status)) {
             ok = false;
@@ -259,23 +304,22 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
           tc_fence_after();
           if (live) {
 #pragma unroll
-            for (int c = 0; c < PCols; c += 32) {
-              uint32_t p0[16], p1[16];
-              tmem_ld16(tbase + sb * PBN + c, p0);
-              tmem_ld16(tbase + sb * PBN + c + 16, p1);
+            for (int c = 0; c < PCols; c += 64) {
+              uint32_t p[4][16];
+#pragma unroll
+              for (int l = 0; l < 4; ++l) tmem_ld16(tbase + sb * PBN + c + 16 * l, p[l]);
               tmem_wait_ld();
-              if (c + 32 == PCols) {  // the slice is in registers: hand the buffer back
+              if (c + 64 == PCols) {  // the slice is in registers: hand the buffer back
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[sb]);
               }
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                fma2(acc[c + i], acc[c + i + 1], __uint_as_float(p0[i]),
-                     __uint_as_float(p0[i + 1]), cur[j]);
-                fma2(acc[c + 16 + i], acc[c + 17 + i], __uint_as_float(p1[i]),
-                     __uint_as_float(p1[i + 1]), cur[j]);
-              }
+              for (int l = 0; l < 4; ++l)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                  fma2(acc[c + 16 * l + i], acc[c + 16 * l + i + 1], __uint_as_float(p[l][i]),
+                       __uint_as_float(p[l][i + 1]), sc);
             }
           } else {
             __syncwarp();
@@ -363,38 +407,72 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inverse) {
   return make_uint2(w[0], w[1]);
 }
 
-// Rows [rows, cols], cols a multiple of 16: one half-warp per 1x128 tile, 8
-// values per lane; lanes past the last column hold zeros.
+// Rows [rows, cols], cols a multiple of 16: a half-warp takes a 1x128 tile, 8
+// values per lane (lanes past the last column hold zeros), four tiles at a time:
+// four loads a lane are in flight, and lane j of the half computes tile j's
+// scale for all.  The max-abs is taken on packed bf16 pairs (exact).  The
+// tile's row and block advance by constants; one division at the start.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {  // of a (>= 0) and |b|
+  b &= 0x7fff7fffu;
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 template <bool kE5M2>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16* __restrict__ x,
                                                             long long rows, int cols,
                                                             uint8_t* __restrict__ q,
                                                             float* __restrict__ sc,
                                                             long long sc_ld) {
-  const int tiles_per_row = (cols + QB - 1) / QB;
-  const long long tiles = rows * tiles_per_row;
+  constexpr int kUnroll = 4;
+  const int per_row = (cols + QB - 1) / QB;
   const int l16 = threadIdx.x & 15;
   const long long hw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
   const long long stride = ((long long)gridDim.x * blockDim.x) >> 4;
-  // every half-warp walks the same number of tiles: the shuffles stay converged
-  const long long iters = (tiles + stride - 1) / stride;
-  for (long long it = 0; it < iters; ++it) {
-    const long long tile = hw + it * stride;
-    const bool live = tile < tiles;
-    const long long r = live ? tile / tiles_per_row : 0;
-    const int b = live ? (int)(tile - r * tiles_per_row) : 0;
-    const int c = b * QB + 8 * l16;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const bool inside = live && c < cols;
-    if (inside) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(x + r * cols + c)), v);
-    float amax = 0.f;
+  const int step_b = (int)(stride % per_row);
+  const long long step_r = stride / per_row;
+  long long r = hw / per_row;
+  int b = (int)(hw - r * per_row);
+  // every half-warp of a warp walks the same number of tiles: the shuffles stay
+  // converged (tiles past the end are not live)
+  const long long tiles = rows * per_row;
+  for (long long t0 = (hw & ~1ll); t0 < tiles; t0 += kUnroll * stride) {
+    uint4 raw[kUnroll];
+    long long at[kUnroll];   // this lane's 8 values of tile j: element offset, -1 none
+    long long my_sc = -1;    // lane j < 4: where tile j's scale goes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int j = 0; j < kUnroll; ++j) {
+      raw[j] = make_uint4(0u, 0u, 0u, 0u);
+      const int c = b * QB + 8 * l16;
+      at[j] = r < rows && c < cols ? r * cols + c : -1;
+      if (at[j] >= 0) raw[j] = __ldg(reinterpret_cast<const uint4*>(x + at[j]));
+      if (l16 == j && r < rows) my_sc = (long long)b * sc_ld + r;
+      r += step_r;
+      b += step_b;
+      if (b >= per_row) {
+        b -= per_row;
+        ++r;
+      }
+    }
+    float amax = 0.f;  // lane j < 4: of tile j
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int j = 0; j < kUnroll; ++j) {
+      uint32_t m = max_abs2(max_abs2(max_abs2(max_abs2(0u, raw[j].x), raw[j].y), raw[j].z),
+                            raw[j].w);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (l16 == j)
+        amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
     const TileScale s = tile_scale(amax, kE5M2 ? 57344.f : 448.f);
-    if (inside) *reinterpret_cast<uint2*>(q + r * cols + c) = codes8<kE5M2>(v, s.inverse);
-    if (live && l16 == 0) sc[(long long)b * sc_ld + r] = s.scale;
+    if (my_sc >= 0) sc[my_sc] = s.scale;
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const float inverse = __shfl_sync(0xffffffffu, s.inverse, j, 16);
+      float v[8];
+      bf16x8_to_f32(raw[j], v);
+      if (at[j] >= 0) *reinterpret_cast<uint2*>(q + at[j]) = codes8<kE5M2>(v, inverse);
+    }
   }
 }
 
@@ -480,10 +558,11 @@ int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scal
   a.a_fmt = e5m2 ? kF8E5M2 : kF8E4M3;
   const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E};
   const uint64_t strides[2] = {(uint64_t)k, (uint64_t)k * n};
-  const uint32_t box[3] = {128, dx ? 128u : 64u, 1};
+  const uint32_t box[3] = {128, dx ? 128u : 256u, 1}, box64[3] = {128, 64, 1};
   if (!make_map(&a.tmA, a_codes, U8, 1, a.kdim, R, PBK, 128) ||
       !make_map(&a.tmA32, a_codes, U8, 1, a.kdim, R, PBK, 32) ||
       !make_map_nd(&a.tmB, w, U8, 3, dims, strides, box) ||
+      (!dx && !make_map_nd(&a.tmB64, w, U8, 3, dims, strides, box64)) ||
       (a.cols % 8 == 0 && !make_map_swizzled(&a.tmOut, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                              a.cols, R, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))) {
     note_text("fp8 matmul: tensor-map encoding failed");
@@ -498,7 +577,7 @@ cudaError_t launch_quantize_rows_fp8(const void* x, long long rows, int cols, in
                                      cudaStream_t st) {
   const long long tiles = rows * ((cols + QB - 1) / QB);
   long long blocks = (tiles * 16 + 255) / 256;
-  if (blocks > 148 * 16) blocks = 148 * 16;
+  if (blocks > 148 * 8) blocks = 148 * 8;
   auto kernel = e5m2 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>;
   kernel<<<(int)blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, codes,
                                       scales, sc_ld);
