@@ -555,6 +555,9 @@ cudaError_t launch_pair(const GArgs& a, long long units, cudaStream_t st) {
 int launch_grouped_matmul_bf16(int mode, const void* rows, int R, const int32_t* offsets, int E,
                                const void* w, int n, int k, void* out, void* ws,
                                cudaStream_t st) {
+  if (matmul_is_narrow(R, E, mode == kDx ? k : n))
+    return launch_matmul_narrow(mode == kDx, rows, 0, nullptr, 0, R, offsets, E, w, nullptr, n, k,
+                                out, ws, st);
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   GArgs a{};
   a.offsets = offsets;

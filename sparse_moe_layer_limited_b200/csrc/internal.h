@@ -210,6 +210,13 @@ int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const in
 int launch_grouped_matmul_fp32(int mode, const float* a, const float* b, int R,
                                const int32_t* offsets, int E, int n, int k, float* out, void* ws,
                                cudaStream_t st);
+// Few rows (matmul_narrow.cu): whether a call of R rows, E experts and `cols`
+// output columns runs there, and the launch (a_scales NULL: bf16).
+bool matmul_is_narrow(int R, int E, int cols);
+int launch_matmul_narrow(int dx, const void* rows, int e5m2, const float* a_scales,
+                         long long sa_ld, int R, const int32_t* offsets, int E, const void* w,
+                         const float* w_scales, int n, int k, void* out, void* ws,
+                         cudaStream_t st);
 // Block-scaled FP8 matmul and its quantisers (matmul_fp8.cu).
 int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scales,
                       long long sa_ld, int R, const int32_t* offsets, int E, const void* w,

@@ -541,6 +541,9 @@ cudaError_t launch(const PArgs& a, cudaStream_t st) {
 int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scales, long long sa_ld,
                       int R, const int32_t* offsets, int E, const void* w, const float* w_scales,
                       int n, int k, void* out, void* ws, cudaStream_t st) {
+  if (matmul_is_narrow(R, E, dx ? k : n))
+    return launch_matmul_narrow(dx, a_codes, e5m2, a_scales, sa_ld, R, offsets, E, w, w_scales, n,
+                                k, out, ws, st);
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   PArgs a{};
   a.offsets = offsets;

@@ -63,6 +63,9 @@ RAGGED = [
     ([33, 0, 97, 129, 200, 31], 0, 5, 264, 520),
     ([1] * 40 + [0] * 20 + [2] * 4, 1, 0, 136, 328),
     ([700], 0, 0, 1000, 72),
+    # few rows, a long contraction in either direction: split over clusters
+    ([3], 0, 0, 40, 4104), ([1, 0, 17], 0, 2, 2056, 1032), ([64], 0, 0, 136, 2048),
+    ([65, 2], 1, 1, 520, 1024),
 ]
 
 
@@ -362,6 +365,7 @@ def dequant_blocks(q, s):
 
 
 FP8_CASES = [
+    (None, 7, 144, 10000), (None, 64, 1000, 2064),
     (None, 1, 16, 16), (None, 1, 129, 128), (None, 130, 264, 144), (None, 33, 257, 528),
     (None, 300, 512, 1040), ([5, 0, 131, 1], 0, 72, 48), ([0, 64, 257, 3, 0, 31], 0, 400, 656),
 ]
