@@ -549,7 +549,8 @@ int moe_matmul_fp8_dx(const void* dy_codes, int dy_format, const float* dy_scale
  *   dbias may be NULL.  ws: moe_layer_norm_workspace_size(rows, d) bytes of
  *   scratch, 256-byte aligned; calls that may run at the same time (streams,
  *   graphs) need one each.  The column sums run in a fixed order.
- * Statistics and sums are fp32. */
+ * Statistics and sums are fp32.  A copy that never lands (about 2 s) leaves NaN
+ * in its rows' results. */
 size_t moe_layer_norm_workspace_size(int64_t rows, int d);
 int moe_layer_norm(const void* x, const float* weight, const float* bias, float eps, int64_t rows,
                    int d, int dtype, void* y, float* mean, float* rstd, void* stream);

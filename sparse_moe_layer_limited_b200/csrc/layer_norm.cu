@@ -9,10 +9,9 @@
 //                        the next row loaded while the current one is reduced
 //   wider, rows in whole 16-byte pieces (row_kernel, row_bwd_kernel): a CTA of
 //                        one thread per two pieces works on two rows at a time,
-//                        with one block barrier; each thread copies its own pieces
-//                        of the next four rows asynchronously into shared memory,
-//                        which keeps 115 KB in flight per SM (backward, 7168
-//                        columns) without registers
+//                        with one block barrier, while bulk copies bring the next
+//                        four rows into shared memory (172 KB of ring per SM in
+//                        the backward at 7168 columns)
 //   other widths         128 to 512 threads a row, elements in registers
 //
 // Statistics: each thread takes the mean and the centred square sum of its own
@@ -27,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -176,16 +176,6 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT) layer_norm_kernel(
 }
 
 // ---- rows of 16-byte pieces, one thread per piece -------------------------------------
-// PIECES 16-byte pieces a thread, S rows in the ring (S - 1 of them in flight).
-// A thread reads back only what it copied itself: no barrier guards the ring.
-__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // Two fp32 values in one 64-bit register: the packed instructions (each half
 // rounded as its scalar form) halve the instructions issued per element, which
 // bound these kernels before HBM did.
@@ -221,6 +211,14 @@ __device__ __forceinline__ float both(f32x2 v) {
 }
 
 // A 16-byte piece of a row as pairs.
+__device__ __forceinline__ void bulk_load(const void* smem, const void* gmem, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(smem)),
+      "l"(gmem), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 template <typename T>
 struct Pack {
   static constexpr int N = 16 / sizeof(T), P = N / 2;
@@ -298,64 +296,86 @@ __device__ __forceinline__ void block_sums(const float (*buf)[32], int warps, fl
 }
 
 // A CTA's rows blockIdx.x, blockIdx.x + gridDim.x, .. on their way through the
-// ring: OPS operands of PIECES pieces a thread.  Addresses advance by constants.
+// ring, ROWS at a time: one thread orders whole rows as bulk copies, which land
+// on a barrier per slot.
+// A wait gives up after a second or two: false, and the caller's rows are NaN.
 template <typename T, int OPS, int PIECES, int ROWS, int S>
 struct Ring {
+  const T* src[OPS];
   const uint4* mem;
-  const char* src[OPS];    // this thread's first piece of the next row to fetch
-  size_t row_step;         // bytes from one of the CTA's rows to the next
-  uint32_t base, row_bytes, piece_bytes;  // shared memory
-  uint32_t put, get;       // byte offsets of the slots fetched and read next
-  int left;                // rows to fetch
+  uint64_t* bar;           // [S / ROWS]
+  size_t row_step;         // elements from one of the CTA's rows to the next
+  uint32_t row_bytes, slot_bytes;
+  int rows, fetched, put, get;
+  uint32_t phase;          // parity of the slot to be read next
   bool in[PIECES];         // this thread's piece i exists
-  __device__ __forceinline__ Ring(const uint4* ring, int rows, int d) {
+  __device__ __forceinline__ Ring(const uint4* ring, uint64_t* bars, int n, int d) {
     const int kT = blockDim.x, t = threadIdx.x;
     mem = ring;
-    piece_bytes = (uint32_t)kT * 16;
-    row_bytes = OPS * PIECES * piece_bytes;
-    base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (uint32_t)t * 16;
-    row_step = (size_t)gridDim.x * d * sizeof(T);
-    put = get = 0;
-    left = rows;
+    bar = bars;
+    row_bytes = (uint32_t)d * sizeof(T);
+    slot_bytes = OPS * PIECES * (uint32_t)kT * 16;
+    row_step = (size_t)gridDim.x * d;
+    rows = n;
+    fetched = put = get = 0;
+    phase = 0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) in[i] = (i * kT + t) * (int)(16 / sizeof(T)) < d;
+    if (t == 0) {
+      for (int i = 0; i < S / ROWS; ++i) mbar_init(&bars[i], 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
   }
   __device__ __forceinline__ void operand(int op, const T* p, int d) {
-    src[op] = reinterpret_cast<const char*>(p + (size_t)blockIdx.x * d) + threadIdx.x * 16;
+    src[op] = p + (size_t)blockIdx.x * d;
   }
-  __device__ __forceinline__ void fetch() {  // the next ROWS rows, one group
+  // Thread 0: the next ROWS rows into their slots, which every thread has read.
+  __device__ __forceinline__ void fetch() {
+    const int n = min(ROWS, rows - fetched);
+    if (n > 0) {
+      mbar_arrive_expect_tx(&bar[put], (uint32_t)(n * OPS) * row_bytes);
+      for (int k = 0; k < n; ++k)
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k, --left) {
-      if (left > 0) {
-#pragma unroll
-        for (int op = 0; op < OPS; ++op) {
-#pragma unroll
-          for (int i = 0; i < PIECES; ++i)
-            if (in[i])
-              copy16(base + put + k * row_bytes + (op * PIECES + i) * piece_bytes,
-                     src[op] + i * piece_bytes);
-          src[op] += row_step;
-        }
+        for (int op = 0; op < OPS; ++op)
+          bulk_load(at(put * ROWS + k, op, 0), src[op] + (size_t)(fetched + k) * row_step,
+                    row_bytes, &bar[put]);
+      fetched += n;
+      put = put + 1 == S / ROWS ? 0 : put + 1;
+    }
+  }
+  __device__ __forceinline__ bool wait() {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(&bar[get], phase)) return true;
+      if ((it & 255u) == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > 2000000000ull) return false;
       }
     }
-    copy_commit();
-    put = put == (S - ROWS) * row_bytes ? 0 : put + ROWS * row_bytes;
+  }
+  __device__ __forceinline__ const uint4* at(int slot, int op, int i) const {
+    return mem + ((slot * OPS + op) * PIECES + i) * (int)blockDim.x;
   }
   __device__ __forceinline__ uint4 read(int k, int op, int i) const {
-    return mem[(get + k * row_bytes + (op * PIECES + i) * piece_bytes) / 16 + threadIdx.x];
+    return at(get * ROWS + k, op, i)[threadIdx.x];
   }
   __device__ __forceinline__ void next() {
-    get = get == (S - ROWS) * row_bytes ? 0 : get + ROWS * row_bytes;
+    if (++get == S / ROWS) {
+      get = 0;
+      phase ^= 1u;
+    }
   }
 };
 
 // ROWS rows at a time: their reductions overlap, and a reduction's instructions
-// are shared by 16 elements a thread.  8192 x 7168 bf16: forward 54 us (4.3
-// TB/s, 0.66 of the measured copy), backward 101 us with the column sums (3.5
+// are shared by 16 elements a thread.  8192 x 7168 bf16: forward 54 us (4.4
+// TB/s, 0.66 of the measured copy), backward 84 us with the column sums (4.2
 // TB/s); what is left is instruction issue and the wait for a row's reduction.
 // Measured and not taken: 8 elements a thread and one row at a time, a CTA of
-// 896 threads (72 and 116 us); one row at a time in two CTAs an SM (57 and
-// 100 us).
+// 896 threads (72 and 116 us); one row at a time in two CTAs an SM (52 and
+// 100 us); 16-byte copies by every thread (54 and 96 us).
 template <typename T, int PIECES, int ROWS, int S>
 __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
     const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, float eps,
@@ -365,24 +385,12 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
   extern __shared__ uint4 ring[];        // [S][PIECES][kT]
   __shared__ float part[2][ROWS][3][32];   // count, mean, M2 of each warp
   const int kT = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, warps = kT >> 5;
-  const long long step = gridDim.x;
-  auto fetch = [&](long long r, int slot) {
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k)
-      if (r + k * step < R) {
-        const T* src = x + (size_t)(r + k * step) * d;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const int c = (i * kT + t) * V;
-          if (c < d) copy16(static_cast<uint32_t>(__cvta_generic_to_shared(
-                           &ring[((slot + k) * PIECES + i) * kT + t])),
-                       src + c);
-        }
-      }
-    copy_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < S - ROWS; i += ROWS) fetch(blockIdx.x + i * step, i);
+  const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's
+  __shared__ uint64_t bars[S / ROWS];
+  Ring<T, 1, PIECES, ROWS, S> in(ring, bars, rows, d);
+  in.operand(0, x, d);
+  if (t == 0)
+    for (int i = 0; i < S; i += ROWS) in.fetch();
   f32x2 wv[PIECES][P], bv[PIECES][P];  // this thread's columns never change
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
@@ -397,10 +405,10 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
   const float inv_d = 1.f / (float)d;
   // all lanes of the warp hold PIECES whole pieces
   const bool whole = ((PIECES - 1) * kT + (warp + 1) * 32) * V <= d;
-  int slot = 0, flip = 0;
-  for (long long r = blockIdx.x; r < R; r += ROWS * step, flip ^= 1) {
-    fetch(r + (S - ROWS) * step, slot == 0 ? S - ROWS : slot - ROWS);
-    copy_wait<S / ROWS - 1>();
+  int flip = 0;
+  size_t row = blockIdx.x;
+  for (int done = 0; done < rows; done += ROWS, flip ^= 1) {
+    const bool landed = in.wait();
     f32x2 v[ROWS][PIECES][P];
     Stat s[ROWS];
 #pragma unroll
@@ -408,8 +416,8 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
       s[k] = Stat{0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
-        if ((i * kT + t) * V < d) {
-          unpack(ring[((slot + k) * PIECES + i) * kT + t], v[k][i], T{});
+        if (in.in[i]) {
+          unpack(in.read(k, 0, i), v[k][i], T{});
           f32x2 sum = v[k][i][0];
 #pragma unroll
           for (int e = 1; e < P; ++e) sum = add2(sum, v[k][i][e]);
@@ -432,7 +440,7 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
           }
         }
     }
-    slot = slot == S - ROWS ? 0 : slot + ROWS;
+    in.next();
     if (whole) {  // equal counts: the merged mean is the middle of the two
       float n = PIECES * V;
 #pragma unroll
@@ -458,6 +466,7 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
         part[flip][k][2][warp] = s[k].m2;
       }
     __syncthreads();
+    if (t == 0) in.fetch();  // every thread has read these rows' slots
     // the warps' statistics: mean first, then the squares around it.  Lanes
     // 0-15 take the first row, lanes 16-31 the second (ROWS == 1: all lanes)
     constexpr int L = 32 / ROWS;
@@ -483,18 +492,18 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    const float rk1 = rsqrtf(a * inv_d + eps);
+    const float rk1 = landed ? rsqrtf(a * inv_d + eps) : __int_as_float(0x7fffffff);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const long long rk = r + k * step;
-      if (rk >= R) break;
+      if (done + k >= rows) break;
       const float mu = __shfl_sync(0xffffffffu, mk, k * L), rs = __shfl_sync(0xffffffffu, rk1, k * L);
       if (t == 0) {
-        mean[rk] = mu;
-        rstd[rk] = rs;
+        mean[row] = mu;
+        rstd[row] = rs;
       }
       const f32x2 mu2 = pair2(-mu, -mu), rs2 = pair2(rs, rs);
-      T* dst = y + (size_t)rk * d;
+      T* dst = y + row * d;
+      row += gridDim.x;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int c = (i * kT + t) * V;
@@ -507,12 +516,12 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
       }
     }
   }
-  copy_wait<0>();
 }
 
-// One partial row of dw and db per CTA, as below.
-template <typename T, int PIECES, int ROWS, int S>
-__global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
+// One partial row of dw and db per CTA, as below.  kExact: every thread has all
+// its pieces (d = 2 kT pieces), so nothing is predicated.
+template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact>
+__global__ void __launch_bounds__(kThreads) row_bwd_kernel(
     const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ mean, const float* __restrict__ rstd, int R, int d,
     T* __restrict__ dx, float* __restrict__ part) {
@@ -520,20 +529,21 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
   constexpr int V = Pack<T>::N, P = Pack<T>::P;
   extern __shared__ uint4 ring[];  // [S][2][PIECES][kT]
   __shared__ float red[2][2 * ROWS][32];
+  __shared__ uint64_t bars[S / ROWS];
   const int kT = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, warps = kT >> 5;
   const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's
-  Ring<T, 2, PIECES, ROWS, S> in(ring, rows, d);
+  Ring<T, 2, PIECES, ROWS, S> in(ring, bars, rows, d);
   in.operand(0, x, d);
   in.operand(1, dy, d);
-#pragma unroll
-  for (int i = 0; i < S - ROWS; i += ROWS) in.fetch();
+  if (t == 0)
+    for (int i = 0; i < S; i += ROWS) in.fetch();
   f32x2 wv[PIECES][P], aw[PIECES][P], ab[PIECES][P];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int c = (i * kT + t) * V;
 #pragma unroll
     for (int e = 0; e < P; ++e) wv[i][e] = aw[i][e] = ab[i][e] = 0ull;
-    if (c < d) load_f32(w + c, wv[i]);
+    if (kExact || c < d) load_f32(w + c, wv[i]);
   }
   const float inv_d = 1.f / (float)d;
   float mu[ROWS], rs[ROWS];
@@ -555,10 +565,11 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
   char* dst = reinterpret_cast<char*>(dx + (size_t)blockIdx.x * d) + t * 16;
   int flip = 0;
   for (int done = 0; done < rows; done += ROWS, flip ^= 1) {
-    in.fetch();
     float mu1[ROWS], rs1[ROWS];  // the next rows'
     row_stats(done + ROWS, mu1, rs1);
-    copy_wait<S / ROWS - 1>();
+    if (!in.wait())
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) mu[k] = __int_as_float(0x7fffffff);
     f32x2 z[ROWS][PIECES][P], h[ROWS][PIECES][P];
     float sums[2 * ROWS];  // h of each row, then h z of each row
 #pragma unroll
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
         const f32x2 mu2 = pair2(-mu[k], -mu[k]), rs2 = pair2(rs[k], rs[k]);
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
-          if (in.in[i]) {
+          if (kExact || in.in[i]) {
             f32x2 g[P];
             unpack(in.read(k, 0, i), z[k][i], T{});
             unpack(in.read(k, 1, i), g, T{});
@@ -590,6 +601,7 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
     const float mine = warp_sums<2 * ROWS>(sums);
     if (lane % (16 / ROWS) == 0) red[flip][lane / (16 / ROWS)][warp] = mine;
     __syncthreads();
+    if (t == 0) in.fetch();  // every thread has read these rows' slots
     block_sums<2 * ROWS>(red[flip], warps, sums);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -599,13 +611,13 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
       const f32x2 rs2 = pair2(rs[k], rs[k]), a2 = pair2(a, a), c2 = pair2(c, c);
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
-        if (in.in[i]) {
+        if (kExact || in.in[i]) {
 #pragma unroll
           for (int e = 0; e < P; ++e)
             z[k][i][e] = fma2(h[k][i][e], rs2, fma2(z[k][i][e], c2, a2));
-          *reinterpret_cast<uint4*>(dst + i * in.piece_bytes) = pack(z[k][i], T{});
+          *reinterpret_cast<uint4*>(dst + i * kT * 16) = pack(z[k][i], T{});
         }
-      dst += in.row_step;
+      dst += in.row_step * sizeof(T);
     }
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -613,7 +625,6 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_bwd_kernel(
       rs[k] = rs1[k];
     }
   }
-  copy_wait<0>();
   float* prow = part + (size_t)blockIdx.x * 2 * d;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
@@ -865,11 +876,11 @@ cudaError_t rows_launch(const Fwd& a, cudaStream_t st) {
                                                     a.rstd);
   return cudaGetLastError();
 }
-template <typename T, int ROWS, int S>
-cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
+template <typename T, int ROWS, int S, int kThreads, bool kExact>
+cudaError_t rows_launch_bwd(const Bwd& a, cudaStream_t st) {
   const int kT = row_threads(a.d, sizeof(T));
   const size_t smem = (size_t)S * 2 * 2 * kT * 16;
-  auto kernel = row_bwd_kernel<T, 2, ROWS, S>;
+  auto kernel = row_bwd_kernel<T, 2, ROWS, S, kThreads, kExact>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
@@ -877,6 +888,20 @@ cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
       static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.mean, a.rstd, a.R, a.d,
       static_cast<T*>(a.dx), a.part);
   return cudaGetLastError();
+}
+template <typename T, int ROWS, int S>
+cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
+  const int kT = row_threads(a.d, sizeof(T));
+  const bool exact = a.d == 2 * kT * (16 / (int)sizeof(T));
+  if constexpr (ROWS == 2) {
+    // up to 448 threads a thread may have 144 registers instead of 128
+    if (kT <= 448)
+      return exact ? rows_launch_bwd<T, ROWS, S, 448, true>(a, st)
+                   : rows_launch_bwd<T, ROWS, S, 448, false>(a, st);
+    return rows_launch_bwd<T, ROWS, S, 512, false>(a, st);
+  } else {
+    return rows_launch_bwd<T, ROWS, S, 1024, false>(a, st);
+  }
 }
 template <typename T, typename Args>
 cudaError_t rows(const Args& a, cudaStream_t st) {
