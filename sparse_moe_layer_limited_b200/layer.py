@@ -22,11 +22,16 @@ class MoELayer:
 
     fused_combine (BF16 only, not with gather): the combine runs inside
     GEMM2's epilogue (moe_expert_ffn_combine) instead of as its own kernel;
-    the output is bit-identical."""
+    the output is bit-identical.
+
+    norm_w, norm_b [d] fp32 (norm_b optional): a layer norm in front of the
+    layer (moe_layer_norm, norm_eps): routing and experts, the shared one
+    included, read the normalised rows; backward then returns the gradient of
+    the rows before the norm, and of its weight and bias."""
 
     def __init__(self, shape: L.MoEShape, router_w, bias, w13, w2, w13_scales=None,
                  w2_scales=None, gamma: float = 0.001, gather: bool = False,
-                 fused_combine: bool = False):
+                 fused_combine: bool = False, norm_w=None, norm_b=None, norm_eps: float = 1e-5):
         rc = L.check_shape(shape)
         if rc != L.OK:
             raise L.MoEError("moe_check_shape", rc)
@@ -56,9 +61,25 @@ class MoELayer:
         self.y_shared = torch.empty(s.T, s.d, dtype=xdt, device=dev)
         self.y = torch.empty(s.T, s.d, dtype=xdt, device=dev)
         self.ws = torch.zeros(L.workspace_size(s), dtype=torch.uint8, device=dev)
+        if norm_w is None and norm_b is not None:
+            raise ValueError("norm_b needs norm_w")
+        self.norm_w, self.norm_b, self.norm_eps = norm_w, norm_b, float(norm_eps)
+        if norm_w is not None:
+            self.x_norm = torch.empty(s.T, s.d, dtype=xdt, device=dev)
+            self.norm_mean = torch.empty(s.T, dtype=torch.float32, device=dev)
+            self.norm_rstd = torch.empty(s.T, dtype=torch.float32, device=dev)
+
+    def norm(self, x, stream=None):
+        """The layer's rows after the norm in front of it (x itself without one)."""
+        if self.norm_w is None:
+            return x
+        L.moe_layer_norm(x, self.norm_w, self.norm_b, self.norm_eps, self.x_norm, self.norm_mean,
+                         self.norm_rstd, stream)
+        return self.x_norm
 
     def route(self, x, stream=None):
         s = self.shape
+        x = self.norm(x, stream)
         L.moe_route(s, x, self.router_w, self.bias, self.topk_idx, self.topk_gate, self.counts,
                     self.ws, stream)
 
@@ -66,6 +87,7 @@ class MoELayer:
         """y = shared(x) + sum_k gate_k expert_k(x); then (optionally) the bias
         update from this batch's counts.  Returns self.y (overwritten next call)."""
         s = self.shape
+        x = self.norm(x, stream)
         L.moe_route(s, x, self.router_w, self.bias, self.topk_idx, self.topk_gate, self.counts,
                     self.ws, stream)
         L.moe_dispatch(s, x, self.topk_idx, self.counts, self.offsets, self.perm_tok, self.slot,
@@ -77,7 +99,7 @@ class MoELayer:
 
     def experts_and_combine(self, x, stream=None):
         """The expert GEMMs and the COMBINE step (one fused launch pair when
-        fused_combine is set); writes self.y."""
+        fused_combine is set) on the rows after the norm; writes self.y."""
         s = self.shape
         if self.fused_combine:
             L.moe_expert_ffn_combine(s, self.x_perm, self.offsets, self.perm_tok, self.slot,
@@ -108,7 +130,9 @@ class MoELayer:
         w13t, w2t: the transposed weights (moe_transpose_weights).  Returns
         dict(dx [T, d] bf16, drouter [N, d] fp32, dgate [T, K] fp32, and with
         weight_grads dw13, dw2 laid out like w13, w2).  The bias gets no
-        gradient (it only selects experts)."""
+        gradient (it only selects experts).  With a norm in front, x is the
+        layer's input before it, dx is its gradient, and dnorm_w [d] and (with
+        norm_b) dnorm_b [d] fp32 come as well."""
         s = self.shape
         if s.dtype != L.DTYPE_BF16 or self.gather:
             raise ValueError("the layer backward runs in BF16 mode on the x_perm path")
@@ -123,6 +147,7 @@ class MoELayer:
                 dlogit=torch.empty(s.T, s.K, dtype=torch.float32, device=dev),
                 dx_route=torch.empty(s.T, s.d, dtype=torch.float32, device=dev))
         B = self._bwd
+        x_in, x = x, (x if self.norm_w is None else self.x_norm)
         dx = torch.empty(s.T, s.d, dtype=xdt, device=dev)
         drouter = torch.empty(s.N, s.d, dtype=torch.float32, device=dev)
         L.moe_combine_backward(s, dy, self.y_perm, self.slot, self.topk_gate, B["dy_perm"],
@@ -141,6 +166,17 @@ class MoELayer:
                              stream)
         L.moe_dispatch_backward(s, B["dx_perm"], B["dx_shared"], self.slot, B["dx_route"], dx,
                                 stream)
+        if self.norm_w is not None:
+            if "norm" not in B:
+                B["norm"] = torch.empty(L.layer_norm_workspace_size(s.T, s.d), dtype=torch.uint8,
+                                        device=dev)
+            out["dx"] = torch.empty_like(dx)
+            out["dnorm_w"] = torch.empty_like(self.norm_w)
+            if self.norm_b is not None:
+                out["dnorm_b"] = torch.empty_like(self.norm_b)
+            L.moe_layer_norm_backward(dx, x_in, self.norm_w, self.norm_mean, self.norm_rstd,
+                                      out["dx"], out["dnorm_w"], out.get("dnorm_b"), B["norm"],
+                                      stream)
         return out
 
     def capture(self, x, update_bias: bool = True):
