@@ -98,6 +98,20 @@ __device__ __forceinline__ int row_tile(int rows, int tiles) {
   return ((rows + tiles - 1) / tiles + 31) & ~31;
 }
 
+// Tile (m, n) of an expert's unit `local`: blocks of kBlockN N tiles, within a
+// block M tile by M tile.  The pairs at work then share kBlockN tiles of the N
+// operand and as many of the M operand as there are pairs to a block row, in
+// place of the whole N operand.  (8192 x 4096 x 7168 forward under sustained
+// power: 398 us without blocks, 377 with 4, 369 with 8 to 16; weight gradients
+// of 32 experts with 16384 skewed rows: 985 us in a burst without, 905 with 12.)
+constexpr int kBlockN = 12;
+__device__ __forceinline__ void raster(int local, int MT, int NT, int& m, int& n) {
+  const int b = local / (MT * kBlockN), rest = local - b * (MT * kBlockN);
+  const int wide = min(kBlockN, NT - b * kBlockN);
+  m = rest / wide;
+  n = b * kBlockN + rest - m * wide;
+}
+
 // A CTA's N rows of one K block, `half` of them (a multiple of 16, at most
 // 128), in at most two copies: many copies of 16 rows each took 2-3x longer,
 // one box of the next size up moves up to 60% more than needed.
@@ -190,21 +204,23 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
     t.width[1] = 0;
     if constexpr (kMode == kDw) {
       t.g = u / (MT * NT);
-      const int local = u - t.g * (MT * NT);
-      const int m = local / NT;
+      int m, n;
+      raster(u - t.g * (MT * NT), MT, NT, m, n);
       t.m0 = m * GM;
-      t.n0 = (local - m * NT) * GN;
+      t.n0 = n * GN;
       t.width[0] = min(GN, (args.cols - t.n0 + 31) & ~31);
       t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
       t.kb = (t.rows + GBK - 1) / GBK;
-      if (bad && local == 0 && tid == 0) atomicOr(args.status, kErrBadIndex);
+      if (bad && m == 0 && n == 0 && tid == 0) atomicOr(args.status, kErrBadIndex);
     } else {
       t.g = ragged_group(start, args.E, u);
       t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
       const int tiles = (t.rows + GN - 1) / GN, local = u - start[t.g];
       const int runs = (tiles + kShare - 1) / kShare;  // units per M tile
-      const int w = row_tile(t.rows, tiles), t0 = local % runs * kShare;
-      t.m0 = local / runs * GM;
+      int m, n;
+      raster(local, MT, runs, m, n);
+      const int w = row_tile(t.rows, tiles), t0 = n * kShare;
+      t.m0 = m * GM;
       t.n0 = t0 * w;
       t.width[0] = min(w, (t.rows - t.n0 + 31) & ~31);
       if (kShare == 2 && t0 + 1 < tiles) {

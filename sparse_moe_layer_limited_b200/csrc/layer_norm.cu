@@ -5,14 +5,15 @@
 //   dx   = rstd (h - mean(h) - z mean(h z)),  dw = sum_rows dy z,  db = sum_rows dy
 //
 // Both passes are bound by HBM: a row is read once, reduced, and written.
-//   up to 1024 columns   a warp per row, up to 32 elements a lane in registers,
-//                        the next row loaded while the current one is reduced
-//   wider, rows in whole 16-byte pieces (row_kernel, row_bwd_kernel): a CTA of
+//   narrow, or not in whole 16-byte pieces up to 1024 columns: a warp per row,
+//                        up to 32 elements a lane in registers, the next row
+//                        loaded while the current one is reduced
+//   rows in whole 16-byte pieces (row_kernel, row_bwd_kernel): a CTA of
 //                        one thread per two pieces works on two rows at a time,
 //                        with one block barrier, while bulk copies bring the next
 //                        four rows into shared memory (172 KB of ring per SM in
 //                        the backward at 7168 columns)
-//   other widths         128 to 512 threads a row, elements in registers
+//   the other wide ones  128 to 512 threads a row, elements in registers
 //
 // Statistics: each thread takes the mean and the centred square sum of its own
 // elements, and (count, mean, M2) are merged by Chan's update, so a large
@@ -811,10 +812,16 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
   }
 }
 
-// The row kernels take rows of whole 16-byte pieces, wider than a warp's, two
-// pieces a thread.  Up to 16 KB a row: two rows at a time, a ring of six; up to
-// 32 KB: one at a time, a ring of three (what fits in shared memory).
-bool by_rows(int d, int elem) { return d > 1024 && d % (16 / elem) == 0 && d * elem <= 32768; }
+// The row kernels take rows of whole 16-byte pieces, two pieces a thread.  Up to
+// 16 KB a row: two rows at a time, a ring of six; up to 32 KB: one at a time, a
+// ring of three (what fits in shared memory).  Narrower than `from` columns a
+// warp per row holds its elements in registers: forward 512 (100000 x 320 bf16
+// 60 us against 70, 30000 x 512 21 against 17), backward 257 (100000 x 320 113
+// us against 80, 16384 x 1024 38 against 34).
+constexpr int kFwdFrom = 512, kBwdFrom = 257;
+bool by_rows(int d, int elem, int from) {
+  return d >= from && d % (16 / elem) == 0 && d * elem <= 32768;
+}
 int row_threads(int d, int elem) { return ((d / (16 / elem) + 1) / 2 + 31) / 32 * 32; }
 int rows_per_sm(int d, int elem) {  // CTAs of a row kernel on an SM: 512 threads in all
   const int t = row_threads(d, elem);
@@ -822,14 +829,15 @@ int rows_per_sm(int d, int elem) {  // CTAs of a row kernel on an SM: 512 thread
 }
 // CTAs of the backward kernel = partial rows.
 int bwd_ctas(int R, int d, int elem) {
-  const bool rows = by_rows(d, elem);
-  const int groups = d <= 1024 ? 4 : 1;
+  const bool rows = by_rows(d, elem, kBwdFrom);
+  const int groups = !rows && d <= 1024 ? 4 : 1;
   const long long want = ((long long)R + groups - 1) / groups;
   const long long most = 148LL * (rows ? rows_per_sm(d, elem) : 2);
   return (int)(want < most ? (want < 1 ? 1 : want) : most);
 }
 
 struct Fwd {
+  static constexpr int kFrom = kFwdFrom;
   const void* x;
   const float *w, *b;
   float eps;
@@ -838,6 +846,7 @@ struct Fwd {
   float *mean, *rstd;
 };
 struct Bwd {
+  static constexpr int kFrom = kBwdFrom;
   const void *dy, *x;
   const float *w, *mean, *rstd;
   int R, d;
@@ -909,21 +918,26 @@ cudaError_t rows(const Args& a, cudaStream_t st) {
   return rows_launch<T, 1, 3>(a, st);
 }
 
-// Threads per row and elements per thread by width: as few threads as hold the
-// row in 32 elements each, fewer elements for short rows.
+// Elements in registers: as few threads per row as hold it in 32 elements each,
+// fewer elements for short rows.  Aligned rows come here where they are narrow,
+// or (fp32) wider than the row kernels take.
 template <typename T, int VEC, typename Args>
 void by_width(const Args& a, cudaStream_t st) {
-  if (a.d <= 256) go<T, VEC, 8 / VEC, 32>(a, st);
-  else if (a.d <= 512) go<T, VEC, 16 / VEC, 32>(a, st);
-  else if (a.d <= 1024) go<T, VEC, 32 / VEC, 32>(a, st);
-  else if (a.d <= 2048) go<T, VEC, 16 / VEC, 128>(a, st);
-  else if (a.d <= 4096) go<T, VEC, 32 / VEC, 128>(a, st);
-  else if (a.d <= 8192) go<T, VEC, 32 / VEC, 256>(a, st);
-  else go<T, VEC, 32 / VEC, 512>(a, st);
+  if (a.d <= 256) return go<T, VEC, 8 / VEC, 32>(a, st);
+  if constexpr (VEC == 1 || Args::kFrom > 257) {
+    if (a.d <= 512) return go<T, VEC, 16 / VEC, 32>(a, st);
+  }
+  if constexpr (VEC == 1) {
+    if (a.d <= 1024) return go<T, VEC, 32, 32>(a, st);
+    if (a.d <= 2048) return go<T, VEC, 16, 128>(a, st);
+    if (a.d <= 4096) return go<T, VEC, 32, 128>(a, st);
+    if (a.d <= 8192) return go<T, VEC, 32, 256>(a, st);
+  }
+  if constexpr (VEC == 1 || sizeof(T) == 4) go<T, VEC, 32 / VEC, 512>(a, st);
 }
 template <typename Args>
 cudaError_t by_type(const Args& a, int dtype, cudaStream_t st) {
-  if (by_rows(a.d, (int)dtype_bytes(dtype)))
+  if (by_rows(a.d, (int)dtype_bytes(dtype), Args::kFrom))
     return dtype == MOE_DTYPE_BF16 ? rows<__nv_bfloat16>(a, st) : rows<float>(a, st);
   if (dtype == MOE_DTYPE_BF16) {
     if (a.d % 8 == 0) by_width<__nv_bfloat16, 8>(a, st);

@@ -71,7 +71,7 @@ int fp8(int dx, const void* a_codes, int a_format, const float* a_scales, int64_
 int check_norm(int64_t rows, int d, int dtype) {
   if (rows < 0 || d <= 0) return MOE_ERR_ARG;
   if (dtype != MOE_DTYPE_FP32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (d > layer_norm_max_d() || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (d > layer_norm_max_d() || rows > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
