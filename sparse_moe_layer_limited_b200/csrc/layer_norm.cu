@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -177,35 +178,6 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT) layer_norm_kernel(
 }
 
 // ---- rows of 16-byte pieces, one thread per piece -------------------------------------
-// Two fp32 values in one 64-bit register: the packed instructions (each half
-// rounded as its scalar form) halve the instructions issued per element, which
-// bound these kernels before HBM did.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair2(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 split2(f32x2 v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float both(f32x2 v) {
   const float2 f = split2(v);
   return f.x + f.y;
