@@ -12,11 +12,14 @@
 // a thread, while the next slice fills the other buffer.  The scales are read
 // from global memory two slices ahead.  The result is rounded once to bf16.
 //
-// 8192 x 4096 x 7168: 245 us at 1.8 GHz (1.96 PFLOP/s), 286 us under sustained
-// power.  Of a slice's 1100 cycles 512 are MMA; without the promotion's reads
-// of TMEM the kernel takes 197 us, with half the operand traffic as well 170
-// us, without the multiply-adds no less than with them.  Measured and not
-// taken: CTA pairs (a third less operand traffic: 240 us dense, but 256-row
+// 8192 x 4096 x 7168: 245 us at 1.8 GHz (1.96 PFLOP/s), 293 us under sustained
+// power; 16411 skewed rows of 64 experts, input gradient, 2048 x 7168: 380 and
+// 445 us.  Of a slice's 1100 cycles 512 are MMA; without the promotion's reads
+// of TMEM the first takes 197 us, with half the operand traffic as well 170 us,
+// without the multiply-adds no less than with them.  The next unit and its
+// first scales are looked up before a unit is stored, in 32-column pieces
+// through two buffers (before that the second case took 398 us).  Measured and
+// not taken: CTA pairs (a third less operand traffic: 240 us dense, but 256-row
 // tiles cost ragged experts 25%).
 //
 // Also here: the quantisers that make the codes, per 1x128 tile of a row and
@@ -40,7 +43,7 @@ constexpr int PABytes = PBM * PBK;
 constexpr int PStageBytes = PABytes + PBN * PBK;
 constexpr int PEpiWarps = 8;
 constexpr int PThreads = 128 + 32 * PEpiWarps;  // a warpgroup of control warps, two of epilogue
-constexpr int PStg = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
+constexpr int PStg = 4096;      // per epilogue warp: two pieces of 32 rows x 32 bf16
 constexpr int PCols = PBN / 2;  // columns per epilogue warp
 constexpr int kAhead = 2;       // slices whose scales are loaded together
 
@@ -54,7 +57,7 @@ struct alignas(64) PArgs {
   CUtensorMap tmA32;  // the same, box {128, 32}
   CUtensorMap tmB;    // weight codes [E, n, k]: fwd box {128, 256, 1}, dx box {128, 128, 1}
   CUtensorMap tmB64;  // fwd: box {128, 64, 1}, for a narrow last column tile
-  CUtensorMap tmOut;  // out [R, cols] bf16, box {64, 32} (cols % 8 == 0)
+  CUtensorMap tmOut;  // out [R, cols] bf16, box {32, 32} (cols % 8 == 0)
   const int32_t* offsets;
   const float* sa;  // [KB, sa_ld]
   const float* sw;  // [E, ceil(n/128), ceil(k/128)]
@@ -135,10 +138,10 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
     return t;
   };
 
-  // 384 threads launch with 168 registers each; the control warps hand 96 of
-  // theirs to the epilogue: 128 * 72 + 256 * 216 = 384 * 168
+  // 384 threads launch with 168 registers each; the control warps hand 112 of
+  // theirs to the epilogue: 128 * 56 + 256 * 224 = 384 * 168
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---- TMA producer: the warp walks the loop together, so that addresses stay
       // warp-uniform, and one lane issues ----
@@ -249,48 +252,61 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---- promotion and epilogue: two warps per lane quadrant, 128 columns each ----
     const int q = warp & 3, half = (warp - 4) >> 2;
     uint8_t* stg = staging + (size_t)(warp - 4) * PStg;
     const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + half * PCols;
     const bool tma_out = (args.cols & 7) == 0;
     uint32_t slice = 0;
+    int buf = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit t = decode(u);
-      const int r0 = t.m * PBM + q * 32, left = t.rows - r0;
-      const int col0 = t.n * PBN + half * PCols;
-      const bool live = left > 0 && col0 < args.cols;  // warp-uniform
+    // the unit at hand, as this warp sees it
+    struct View {
+      int r0, left, col0;  // its first row of the expert, the rows from there, its first column
+      bool live;           // it has rows and columns (the same for the whole warp)
+      const float *sa, *sw;
+    };
+    const int sw_step = kDx ? args.kb : 1;
+    auto view = [&](const Unit& t) {
+      View v;
+      v.r0 = t.m * PBM + q * 32;
+      v.left = t.rows - v.r0;
+      v.col0 = t.n * PBN + half * PCols;
+      v.live = v.left > 0 && v.col0 < args.cols;
       // scales: sa[kb][row], and the weight block of this warp's columns
-      const int row = min(t.first + r0 + lane, args.R - 1);
-      const float* sa = args.sa + row;
-      const float* sw = args.sw + (size_t)t.g * args.nb * args.kb +
-                        (kDx ? (size_t)(col0 / 128) : (size_t)(col0 / 128) * args.kb);
-      const int sw_step = kDx ? args.kb : 1;
+      v.sa = args.sa + min(t.first + v.r0 + lane, args.R - 1);
+      v.sw = args.sw + (size_t)t.g * args.nb * args.kb +
+             (kDx ? (size_t)(v.col0 / 128) : (size_t)(v.col0 / 128) * args.kb);
+      return v;
+    };
+    // loaded kAhead slices ahead (a unit's first ones before the unit before it
+    // is stored), multiplied when used
+    float row_sc[kAhead], w_sc[kAhead], row_nx[kAhead], w_nx[kAhead];
+    auto scales = [&](const View& v, int kb) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        row_nx[j] = w_nx[j] = 0.f;
+        if (v.live && kb + j < KB) {
+          row_nx[j] = __ldg(v.sa + (size_t)(kb + j) * args.sa_ld);
+          w_nx[j] = __ldg(v.sw + (size_t)(kb + j) * sw_step);
+        }
+      }
+    };
+    Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
+    View v = view(t);
+    if (blockIdx.x < total) scales(v, 0);
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
       float acc[PCols];
 #pragma unroll
       for (int i = 0; i < PCols; ++i) acc[i] = 0.f;
-      // loaded kAhead slices ahead, multiplied when used
-      float row_sc[kAhead], w_sc[kAhead], row_nx[kAhead], w_nx[kAhead];
-      auto scales = [&](float (&r)[kAhead], float (&q)[kAhead], int kb) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          r[j] = q[j] = 0.f;
-          if (live && kb + j < KB) {
-            r[j] = __ldg(sa + (size_t)(kb + j) * args.sa_ld);
-            q[j] = __ldg(sw + (size_t)(kb + j) * sw_step);
-          }
-        }
-      };
-      scales(row_nx, w_nx, 0);
       for (int kb = 0; kb < KB && ok; kb += kAhead) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           row_sc[j] = row_nx[j];
           w_sc[j] = w_nx[j];
         }
-        scales(row_nx, w_nx, kb + kAhead);
+        if (kb + kAhead < KB) scales(v, kb + kAhead);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           if (kb + j >= KB) break;
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
           }
           ++slice;
           tc_fence_after();
-          if (live) {
+          if (v.live) {
 #pragma unroll
             for (int c = 0; c < PCols; c += 64) {
               uint32_t p[4][16];
@@ -328,45 +344,56 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
         }
       }
       if (!ok) break;
-      if (!live) continue;
+      const Unit done = t;
+      const View d = v;
+      if (u + (int)gridDim.x < total) {
+        t = decode(u + gridDim.x);
+        v = view(t);
+        scales(v, 0);
+      }
+      if (!d.live) continue;
+      // 32 columns at a time through two staging buffers (64-byte rows, their
+      // 16-byte chunks swizzled as the store reads them)
 #pragma unroll
-      for (int c = 0; c < PCols; c += 64) {
-        const int col = col0 + c;
+      for (int c = 0; c < PCols; c += 32, buf ^= 1) {
+        const int col = d.col0 + c;
         if (col >= args.cols) break;
-        const bool by_tma = tma_out && left >= 32;
-        if (lane == 0) bulk_wait_read_all();  // the previous piece has left the buffer
+        uint8_t* tile = stg + buf * (PStg / 2);
+        if (lane == 0) bulk_wait_read_but_one();  // this buffer's last store has read it
         __syncwarp();
-        uint8_t* my = stg + lane * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float* a = acc + c + 8 * j;
-          const uint4 v = make_uint4(bf16x2_bits(a[0], a[1]), bf16x2_bits(a[2], a[3]),
-                                     bf16x2_bits(a[4], a[5]), bf16x2_bits(a[6], a[7]));
-          *reinterpret_cast<uint4*>(my + ((j ^ (lane & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(bf16x2_bits(a[0], a[1]), bf16x2_bits(a[2], a[3]),
+                         bf16x2_bits(a[4], a[5]), bf16x2_bits(a[6], a[7]));
         }
-        if (by_tma) {
+        if (tma_out && d.left >= 32) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&args.tmOut, stg, col, t.first + r0);
+            tma_store_2d(&args.tmOut, tile, col, done.first + d.r0);
             bulk_commit_group();
           }
-        } else {
-          // ragged last rows, or rows that do not start on 16 bytes: the warp
-          // writes one row's 64 columns at a time
-          __syncwarp();
-          const int rows = min(32, left), wide = min(64, args.cols - col);
-          for (int i = 0; i < rows; ++i) {
-            __nv_bfloat16* dst =
-                args.out + (size_t)(t.first + r0 + i) * (size_t)args.cols + col;
-            for (int e = lane; e < wide; e += 32) {
-              const int piece = (e >> 3) ^ (i & 7);
-              dst[e] = *reinterpret_cast<const __nv_bfloat16*>(stg + i * 128 + piece * 16 +
-                                                               (e & 7) * 2);
-            }
-          }
-          __syncwarp();
+          continue;
         }
+        __syncwarp();
+        const int rows = min(32, d.left);
+        __nv_bfloat16* dst = args.out + (size_t)(done.first + d.r0) * (size_t)args.cols + col;
+        if (tma_out) {
+          // the expert's last rows: 16 bytes a lane, 8 rows at a time
+          const int j = lane & 3;
+          for (int i = lane >> 2; i < rows; i += 8)
+            if (col + 8 * j < args.cols)
+              *reinterpret_cast<uint4*>(dst + (size_t)i * args.cols + 8 * j) =
+                  *reinterpret_cast<const uint4*>(tile + i * 64 + ((j ^ ((i >> 1) & 3)) << 4));
+        } else if (col + lane < args.cols) {
+          // rows that do not start on 16 bytes: a column a lane, row by row
+          for (int i = 0; i < rows; ++i)
+            dst[(size_t)i * args.cols + lane] = *reinterpret_cast<const __nv_bfloat16*>(
+                tile + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+        }
+        __syncwarp();
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -525,7 +552,7 @@ cudaError_t launch(const PArgs& a, cudaStream_t st) {
   const size_t smem = fp8_mm_smem(a.E);
   cudaError_t e = note_cuda(cudaFuncSetAttribute(matmul_fp8_kernel<kDx>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem),
+                                                 (int)fp8_mm_smem(kMatmulMaxGroups)),
                             "fp8 matmul: set shared-memory size");
   if (e != cudaSuccess) return e;
   const long long mt = a.R / PBM + (a.R < a.E ? a.R : a.E);  // no more row tiles than this
@@ -567,7 +594,7 @@ int launch_matmul_fp8(int dx, int e5m2, const void* a_codes, const float* a_scal
       !make_map_nd(&a.tmB, w, U8, 3, dims, strides, box) ||
       (!dx && !make_map_nd(&a.tmB64, w, U8, 3, dims, strides, box64)) ||
       (a.cols % 8 == 0 && !make_map_swizzled(&a.tmOut, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                                             a.cols, R, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))) {
+                                             a.cols, R, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))) {
     note_text("fp8 matmul: tensor-map encoding failed");
     return MOE_ERR_CUDA;
   }
