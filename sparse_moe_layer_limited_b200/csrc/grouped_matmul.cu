@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
                 bulk_commit_group();
               }
             } else {
-              // the expert's last rows: 16 bytes a lane, 8 rows at a time
+              // the expert's last rows: 16 bytes a lane, 8 rows at a time.  Their
+              // piece is an empty group: the buffers' turns are counted in groups
+              if (lane == 0) bulk_commit_group();
               __syncwarp();
               const int c = (lane & 3) * 8;
               for (int i = lane >> 2; i < left; i += 8)

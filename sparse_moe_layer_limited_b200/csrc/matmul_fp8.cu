@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
           }
           continue;
         }
+        if (lane == 0) bulk_commit_group();  // the buffers' turns are counted in groups
         __syncwarp();
         const int rows = min(32, d.left);
         __nv_bfloat16* dst = args.out + (size_t)(done.first + d.r0) * (size_t)args.cols + col;

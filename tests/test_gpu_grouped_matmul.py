@@ -242,6 +242,51 @@ def test_long_rows_pass_32_bit_offsets(M, ws):
     assert not y[0].any() and not y[R - 151].any()
 
 
+@pytest.mark.parametrize("kind", ["fwd", "dx", "dw", "fp8"])
+def test_short_contractions_of_many_ragged_units(M, ws, kind):
+    """Units that end within microseconds of each other, full row blocks (stored by bulk copies)
+    next to ragged ones (stored by the threads): a staging buffer handed on too early shows as
+    32 x 32 blocks of another tile's values, in some runs only."""
+    g = gen(20)
+    counts, n, k = [674, 633, 680, 632, 678, 659], 4152, 168
+    if kind == "fp8":
+        n, k = 4152, 80
+    off, R, E = offsets_of(counts), sum(counts), len(counts)
+    if kind == "dx":
+        n, k = k, n
+    x, dy, w = rand(g, R, k, dtype=BF), rand(g, R, n, dtype=BF), rand(g, E, n, k, dtype=BF)
+    if kind == "fp8":
+        qa, sa = torch.empty(R, k, dtype=E4M3, device="cuda"), torch.empty(1, R, device="cuda")
+        qw = torch.empty(E, n, k, dtype=E4M3, device="cuda")
+        sw = torch.empty(E, -(-n // 128), 1, device="cuda")
+        M.moe_quantize_rows_fp8(x, qa, sa)
+        M.moe_quantize_blocks_fp8(w, qw, sw)
+        out = torch.empty(R, n, dtype=BF, device="cuda")
+        call = lambda: M.moe_matmul_fp8(qa, sa, off, qw, sw, out, ws)  # noqa: E731
+        want, mag = expected("fwd", dequant_rows(qa, sa), dequant_blocks(qw, sw), counts, 0, n, k)
+        K = k + 2
+    elif kind == "dw":
+        out = torch.empty(E, n, k, dtype=BF, device="cuda")
+        call = lambda: M.moe_grouped_matmul_dw(dy, x, off, out, ws)  # noqa: E731
+        want, mag = expected("dw", dy, x, counts, 0, n, k)
+        K = max(counts)
+    else:
+        out = torch.empty(R, n if kind == "fwd" else k, dtype=BF, device="cuda")
+        f = M.moe_grouped_matmul if kind == "fwd" else M.moe_grouped_matmul_dx
+        a = x if kind == "fwd" else dy
+        call = lambda: f(a, off, w, out, ws)  # noqa: E731
+        want, mag = expected(kind, a, w, counts, 0, n, k)
+        K = k if kind == "fwd" else n
+    first = None
+    for _ in range(60):
+        out.fill_(7.0)
+        call()
+        if first is None:
+            first = out.clone()
+            close(first, want, mag, K)
+        assert torch.equal(out, first)
+
+
 def test_side_stream_and_graphs_sharing_a_workspace(M, ws):
     g = gen(9)
     counts, n, k = [17, 200], 128, 256
