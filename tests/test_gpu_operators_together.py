@@ -151,3 +151,61 @@ def test_a_normed_fp8_projection_and_its_gradients(M):
         assert S.rel_fro(got.double().cpu().numpy(), ref.cpu().numpy()) <= tol
     assert M.moe_read_device_status(ws) == 0
     assert np.isfinite(y.float().cpu().numpy()).all()
+
+
+def test_calls_on_several_streams_at_once(M):
+    """Every operator on its own stream, all sharing one status workspace, many times over: the
+    results are those of calls made one after another."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *sh, dt=BF: torch.randn(*sh, generator=g, device="cuda").to(dt)  # noqa: E731
+    ws = torch.zeros(M.matmul_workspace_size(), dtype=torch.uint8, device="cuda")
+    counts = [300, 0, 41, 513, 7, 260]
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    R, E, n, k = sum(counts), len(counts), 1160, 392
+    x, dy, w = rnd(R, k), rnd(R, n), rnd(E, n, k)
+    x32, w32 = x.float(), w.float()
+    E4 = torch.float8_e4m3fn
+    xq, xs = torch.empty(R, 400, dtype=E4, device="cuda"), torch.empty(4, R, device="cuda")
+    x400, w400 = rnd(R, 400), rnd(E, n, 400)
+    wq = torch.empty(E, n, 400, dtype=E4, device="cuda")
+    wsc = torch.empty(E, -(-n // 128), 4, device="cuda")
+    M.moe_quantize_blocks_fp8(w400, wq, wsc)
+    few = rnd(3, k)
+    d = 1536
+    nx, nw, ndy = rnd(700, d), rnd(d, dt=torch.float32), rnd(700, d)
+    mean, rstd = torch.empty(700, device="cuda"), torch.empty(700, device="cuda")
+    lws = torch.empty(M.layer_norm_workspace_size(700, d), dtype=torch.uint8, device="cuda")
+    e = lambda *sh, dt=BF: torch.empty(*sh, dtype=dt, device="cuda")  # noqa: E731
+    y, dx, dw, y32, y8, yf = (e(R, n), e(R, k), e(E, n, k), e(R, n, dt=torch.float32), e(R, n),
+                              e(3, n))
+    ny, ndx, ndw = e(700, d), e(700, d), e(d, dt=torch.float32)
+
+    def fp8(st):
+        M.moe_quantize_rows_fp8(x400, xq, xs, st)
+        M.moe_matmul_fp8(xq, xs, off, wq, wsc, y8, ws, st)
+
+    def norm(st):
+        M.moe_layer_norm(nx, nw, None, 1e-5, ny, mean, rstd, st)
+        M.moe_layer_norm_backward(ndy, nx, nw, mean, rstd, ndx, ndw, None, lws, st)
+    jobs = [(lambda st: M.moe_grouped_matmul(x, off, w, y, ws, st), [y]),
+            (lambda st: M.moe_grouped_matmul_dx(dy, off, w, dx, ws, st), [dx]),
+            (lambda st: M.moe_grouped_matmul_dw(dy, x, off, dw, ws, st), [dw]),
+            (lambda st: M.moe_grouped_matmul(x32, off, w32, y32, ws, st), [y32]),
+            (lambda st: M.moe_grouped_matmul(few, None, w[:1], yf, ws, st), [yf]),
+            (fp8, [y8]), (norm, [ny, ndx, ndw])]
+    alone = []
+    for job, outs in jobs:
+        job(None)
+        alone.append([t.clone() for t in outs])
+        for t in outs:
+            t.fill_(3.0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(25):
+        for (job, _o), st in zip(jobs, streams):
+            job(st)
+    torch.cuda.synchronize()
+    for (_j, outs), want in zip(jobs, alone):
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+    assert M.moe_read_device_status(ws) == 0
