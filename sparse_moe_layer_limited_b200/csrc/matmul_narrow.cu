@@ -11,6 +11,11 @@
 // order (every CTA takes its share of the rows), through distributed shared
 // memory.  No workspace, no atomics.
 //
+// Measured: one row of 2048 x 7168 bf16 17 us (27 on the pair kernel), 8 rows on
+// 8 experts of 2048 x 7168 45 us (5.3 TB/s of weights), FP8 7 rows of 7168 x 2048
+// 9.6 us (14.8), 64 rows of 4096 x 7168 17 us (31); 6-7 us of each are start and
+// end (tensor memory, barriers, first copies, the cluster's two barriers).
+//
 // FP8: every 128-wide slice is one product into its own TMEM buffer (eight of
 // 64 columns in flight), multiplied by sa[row] * sw and added to fp32 registers.
 // All 128 output columns of a unit lie in one weight block, so the factor
