@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
     uint32_t tissued = 0, tphase = 0;  // last blocks: per stage, parity of the next use
     bool ok = true;
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);  // the leader's barriers
-    Unit t = decode(pair < total ? pair : 0);
+    Unit t{};
+    if (pair < total) t = decode(pair);
     for (int u = pair; u < total && ok; u += npairs) {
       const int mrow = t.m0 + (int)rank * kHalf;
       Unit next = t;
@@ -357,7 +358,8 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       uint32_t phase = 0, tphase = 0;
       int use = 0;  // accumulator uses so far
       bool ok = true;
-      Unit t = decode(pair < total ? pair : 0);
+      Unit t{};
+      if (pair < total) t = decode(pair);
       for (int u = pair; u < total && ok; u += npairs) {
         for (int j = 0; j < t.tiles && ok; ++j) {
           const uint32_t ap = (((use + j) >> 1) & 1) ^ 1u;

@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
-      Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
+      Unit t{};
+      if (blockIdx.x < total) t = decode(blockIdx.x);
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
         Unit next = t;
         const int nc = min(PBN / kChunkCols, (args.cols - t.n * PBN + kChunkCols - 1) / kChunkCols);
@@ -214,7 +215,8 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
       int stage = 0;
       uint32_t phase = 0, slice = 0;
       bool ok = true;
-      Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
+      Unit t{};
+      if (blockIdx.x < total) t = decode(blockIdx.x);
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
         Unit next = t;
         const int width = min(PBN, args.cols - t.n * PBN);
@@ -293,9 +295,13 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
         }
       }
     };
-    Unit t = decode(blockIdx.x < total ? blockIdx.x : 0);
-    View v = view(t);
-    if (blockIdx.x < total) scales(v, 0);
+    Unit t{};
+    if (blockIdx.x < total) t = decode(blockIdx.x);
+    View v{};
+    if (blockIdx.x < total) {
+      v = view(t);
+      scales(v, 0);
+    }
     for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
       float acc[PCols];
 #pragma unroll

@@ -206,6 +206,64 @@ def test_no_rows(M, ws):
     assert (dw == 0).all()
 
 
+def test_rows_that_belong_to_nobody(M, ws):
+    """Many rows, no owner: nothing is written but the (zero) weight gradients, on the kernels for
+    many rows too."""
+    R, E, n, k = 40000, 3, 512, 64
+    off = torch.full((E + 1,), 17, dtype=torch.int32, device="cuda")
+    x = torch.full((R, k), float("nan"), dtype=BF, device="cuda")
+    w = torch.ones(E, n, k, dtype=BF, device="cuda")
+    y = torch.full((R, n), 7.0, dtype=BF, device="cuda")
+    M.moe_grouped_matmul(x, off, w, y, ws)
+    assert (y == 7.0).all()
+    dx = torch.full((R, k), 7.0, dtype=BF, device="cuda")
+    M.moe_grouped_matmul_dx(y, off, w, dx, ws)
+    assert (dx == 7.0).all()
+    M.moe_grouped_matmul_dw(y, x, off, w, ws)
+    assert (w == 0).all()
+    q = torch.zeros(R, k, dtype=E4M3, device="cuda")
+    wq = torch.zeros(E, n, k, dtype=E4M3, device="cuda")
+    M.moe_matmul_fp8(q, torch.ones(1, R, device="cuda"), off, wq, torch.ones(E, 4, 1, device="cuda"),
+                     y, ws)
+    assert (y == 7.0).all()
+
+
+@pytest.mark.parametrize("rows_each", [1, 40])
+def test_the_most_experts(M, ws, rows_each):
+    g = gen(21)
+    counts = [rows_each * (e % 3) for e in range(384)]
+    R, n, k = sum(counts), 264, 72
+    off = offsets_of(counts)
+    x, dy, w = rand(g, R, k, dtype=BF), rand(g, R, n, dtype=BF), rand(g, 384, n, k, dtype=BF)
+    y, dx, dw = (torch.empty(R, n, dtype=BF).cuda(), torch.empty(R, k, dtype=BF).cuda(),
+                 torch.empty(384, n, k, dtype=BF).cuda())
+    M.moe_grouped_matmul(x, off, w, y, ws)
+    M.moe_grouped_matmul_dx(dy, off, w, dx, ws)
+    M.moe_grouped_matmul_dw(dy, x, off, dw, ws)
+    close(y, *expected("fwd", x, w, counts, 0, n, k), k)
+    close(dx, *expected("dx", dy, w, counts, 0, n, k), n)
+    close(dw, *expected("dw", dy, x, counts, 0, n, k), max(counts))
+
+
+def test_large_graph_replays(M, ws):
+    """The kernels for many rows, first reached inside a capture, replayed with other inputs."""
+    g = gen(22)
+    counts, n, k = [900, 0, 1300, 411], 1024, 640
+    off, R = offsets_of(counts), sum(counts)
+    x, w = rand(g, R, k, dtype=BF), rand(g, 4, n, k, dtype=BF)
+    y, dw = torch.empty(R, n, dtype=BF, device="cuda"), torch.empty_like(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.moe_grouped_matmul(x, off, w, y, ws)
+        M.moe_grouped_matmul_dw(y, x, off, dw, ws)
+    for _ in range(2):
+        x.copy_(rand(g, R, k, dtype=BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        close(y, *expected("fwd", x, w, counts, 0, n, k), k)
+        close(dw, *expected("dw", y, x, counts, 0, n, k), max(counts))
+
+
 def test_bad_offsets_are_reported_and_skipped(M):
     g = gen(7)
     ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
