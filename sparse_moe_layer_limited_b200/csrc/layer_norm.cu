@@ -848,8 +848,10 @@ cudaError_t rows_launch(const Fwd& a, cudaStream_t st) {
   const int kT = row_threads(a.d, sizeof(T));
   const size_t smem = (size_t)S * 2 * kT * 16;
   auto kernel = row_kernel<T, 2, ROWS, S>;
+  // the same opt-in for every width: host threads may call at the same time
+  constexpr int most_smem = S * 2 * (ROWS == 2 ? 512 : 1024) * 16;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       most_smem);
   if (e != cudaSuccess) return e;
   const int most = 148 * rows_per_sm(a.d, sizeof(T));
   kernel<<<a.R < most ? a.R : most, kT, smem, st>>>(static_cast<const T*>(a.x), a.w, a.b, a.eps,
@@ -862,8 +864,9 @@ cudaError_t rows_launch_bwd(const Bwd& a, cudaStream_t st) {
   const int kT = row_threads(a.d, sizeof(T));
   const size_t smem = (size_t)S * 2 * 2 * kT * 16;
   auto kernel = row_bwd_kernel<T, 2, ROWS, S, kThreads, kExact>;
+  constexpr int most_smem = S * 2 * 2 * kThreads * 16;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       most_smem);
   if (e != cudaSuccess) return e;
   kernel<<<bwd_ctas(a.R, a.d, sizeof(T)), kT, smem, st>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.mean, a.rstd, a.R, a.d,

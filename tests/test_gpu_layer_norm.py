@@ -179,3 +179,34 @@ def test_side_stream_and_graph(M):
     torch.cuda.synchronize()
     for a, c in zip((dx, dw, db), kept):
         assert torch.equal(a, c)
+
+
+def test_two_host_threads_with_rows_of_different_widths(M):
+    """Calls of one process at the same time, on streams of their own."""
+    import threading
+    cases, errors = [], []
+    for d in (1032, 6144, 7680):
+        x, w, b, dy = make(40, d, BF, seed=d)
+        cases.append((x, w, b, dy, *forward(M, x, w, b, 1e-5)))
+    torch.cuda.synchronize()
+
+    def work(x, w, b, dy, y, mean, rstd):
+        try:
+            st = torch.cuda.Stream()
+            got = [torch.empty_like(t) for t in (y, mean, rstd)]
+            dx, dw = torch.empty_like(x), torch.empty_like(w)
+            ws = torch.empty(M.layer_norm_workspace_size(*x.shape), dtype=torch.uint8,
+                             device="cuda")
+            for _ in range(3000):
+                M.moe_layer_norm(x, w, b, 1e-5, *got, stream=st)
+                M.moe_layer_norm_backward(dy, x, w, mean, rstd, dx, dw, None, ws, stream=st)
+            st.synchronize()
+            assert all(torch.equal(g, t) for g, t in zip(got, (y, mean, rstd)))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
