@@ -477,7 +477,8 @@ int moe_forward(const moe_shape* shape, const void* x, const float* router_w, fl
  * it.  After MOE_DEV_WAIT_TIMEOUT clear it before the next call.
  *
  * Supported: experts <= 384; for BF16 n and k multiples of 8; for FP8 k (and
- * for the input gradient n) a multiple of 16; else MOE_ERR_UNSUPPORTED.  A
+ * for the input gradient n) a multiple of 16; rows and widths below 2^31 - 65536
+ * and output tiles of 64 x 64 below 2^31; else MOE_ERR_UNSUPPORTED.  A
  * non-positive size, a negative row count, a NULL or misaligned pointer gives
  * MOE_ERR_ARG.  rows = 0 is allowed (x, dy, y, dx may then be NULL). */
 size_t moe_matmul_workspace_size(void);

@@ -441,6 +441,8 @@ def _matrix(t, name, dims):
     shape = t.shape
     if len(shape) != dims:
         raise ValueError(f"{name}: expected {dims} dimensions, got {len(shape)}")
+    if max(shape) > 0x7fffffff:  # ctypes would cut a C int short
+        raise ValueError(f"{name}: dimensions {list(shape)} pass 31 bits")
     return shape
 
 

@@ -16,11 +16,15 @@ cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 int as_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 long long up(long long a, long long b) { return (a + b - 1) / b; }
 
+// Widths up to this: kernels round them up to whole tiles in 31 bits.
+constexpr int kMaxWidth = INT32_MAX - 65536;
+
 // Sizes and groups of a matmul.  offsets == NULL: one group of all rows.
 int check_matmul(int64_t rows, const int32_t* offsets, int experts, int n, int k) {
   if (rows < 0 || experts <= 0 || n <= 0 || k <= 0) return MOE_ERR_ARG;
   if (offsets == nullptr ? experts != 1 : !ok16(offsets)) return MOE_ERR_ARG;
-  if (experts > kMatmulMaxGroups || rows > INT32_MAX - 128) return MOE_ERR_UNSUPPORTED;
+  if (experts > kMatmulMaxGroups || rows > kMaxWidth || n > kMaxWidth || k > kMaxWidth)
+    return MOE_ERR_UNSUPPORTED;
   // output tiles (at least 64 x 64) are numbered in 31 bits, and so are 128-wide blocks
   const long long wide = up(n > k ? n : k, 64);
   if ((rows / 64 + experts) * wide > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -71,7 +75,7 @@ int fp8(int dx, const void* a_codes, int a_format, const float* a_scales, int64_
 int check_norm(int64_t rows, int d, int dtype) {
   if (rows < 0 || d <= 0) return MOE_ERR_ARG;
   if (dtype != MOE_DTYPE_FP32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (d > layer_norm_max_d() || rows > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;
+  if (d > layer_norm_max_d() || rows > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -115,7 +119,7 @@ int moe_quantize_rows_fp8(const void* x, int64_t rows, int cols, int format, uin
                           float* scales, int64_t scale_ld, void* stream) {
   if (rows < 0 || cols <= 0 || scale_ld < rows) return MOE_ERR_ARG;
   if (format != MOE_FP8_E4M3 && format != MOE_FP8_E5M2) return MOE_ERR_UNSUPPORTED;
-  if (cols % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (cols % 16 != 0 || cols > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!ok16(x) || !ok16(codes) || !ok16(scales)) return MOE_ERR_ARG;
   return as_status(launch_quantize_rows_fp8(x, rows, cols, format == MOE_FP8_E5M2, codes, scales,
@@ -125,6 +129,7 @@ int moe_quantize_rows_fp8(const void* x, int64_t rows, int cols, int format, uin
 int moe_quantize_blocks_fp8(const void* w, int experts, int n, int k, uint8_t* codes,
                             float* scales, void* stream) {
   if (experts <= 0 || n <= 0 || k <= 0) return MOE_ERR_ARG;
+  if (n > kMaxWidth || k > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   if (k % 16 != 0 || up(n, 128) * up(k, 128) > INT32_MAX / experts) return MOE_ERR_UNSUPPORTED;
   if (!ok16(w) || !ok16(codes) || !ok16(scales)) return MOE_ERR_ARG;
   return as_status(launch_quantize_blocks_fp8(w, experts, n, k, codes, scales, as_stream(stream)));

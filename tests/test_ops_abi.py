@@ -156,3 +156,30 @@ def test_the_binding_refuses_wrong_tensors(L):
         moe_matmul_fp8(x, torch.zeros(1, 4), off, w, torch.zeros(2, 1, 1), y, ws)
     with pytest.raises(TypeError):
         moe_layer_norm(x.half(), torch.ones(24), None, 1e-5, x, torch.ones(4), torch.ones(4))
+
+
+WIDE = (1 << 31) - 16  # a C int whose rounding up to whole tiles is none
+
+
+def test_widths_next_to_31_bits(L):
+    f = L.lib()
+    U = L.ERR_UNSUPPORTED
+    for n, k in ((WIDE, 16), (16, WIDE)):
+        for dt in (L.DTYPE_BF16, L.DTYPE_FP32):
+            assert f.moe_grouped_matmul(P, 4, N, 1, P, n, k, dt, P, P, N) == U
+            assert f.moe_grouped_matmul_dx(P, 4, N, 1, P, n, k, dt, P, P, N) == U
+            assert f.moe_grouped_matmul_dw(P, P, 4, N, 1, n, k, dt, P, P, N) == U
+        assert f.moe_matmul_fp8(P, 0, P, 4, 4, N, 1, P, P, n, k, P, P, N) == U
+        assert f.moe_matmul_fp8_dx(P, 0, P, 4, 4, N, 1, P, P, n, k, P, P, N) == U
+        assert f.moe_quantize_blocks_fp8(P, 1, n, k, P, P, N) == U
+    assert f.moe_quantize_rows_fp8(P, 4, WIDE, 0, P, P, 4, N) == U
+
+
+def test_dimensions_past_31_bits(L):
+    """A view of that many columns, refused before its memory is looked at."""
+    w = torch.empty(1).expand(1, 8, (1 << 32) + 8)
+    x = torch.empty(1).expand(1, (1 << 32) + 8)
+    with pytest.raises(ValueError, match="31 bits"):
+        L.moe_grouped_matmul(x, None, w, x, x)
+    with pytest.raises(ValueError, match="31 bits"):
+        L.moe_quantize_rows_fp8(x, x, x)
