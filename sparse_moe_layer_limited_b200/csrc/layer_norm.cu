@@ -5,15 +5,13 @@
 //   dx   = rstd (h - mean(h) - z mean(h z)),  dw = sum_rows dy z,  db = sum_rows dy
 //
 // Both passes are bound by HBM: a row is read once, reduced, and written.
-//   narrow, or not in whole 16-byte pieces up to 1024 columns: a warp per row,
-//                        up to 32 elements a lane in registers, the next row
-//                        loaded while the current one is reduced
-//   rows in whole 16-byte pieces (row_kernel, row_bwd_kernel): a CTA of
-//                        one thread per two pieces works on two rows at a time,
-//                        with one block barrier, while bulk copies bring the next
-//                        four rows into shared memory (172 KB of ring per SM in
-//                        the backward at 7168 columns)
-//   the other wide ones  128 to 512 threads a row, elements in registers
+//   rows of whole 16-byte pieces up to 32 KB (row_kernel, row_bwd_kernel): a CTA
+//                        of one thread per two or four pieces, one block barrier
+//                        a reduction, while bulk copies bring the next rows into
+//                        shared memory (172 KB of ring per SM at 7168 columns)
+//   the others           a warp, or 128 to 512 threads, per row, up to 32
+//                        elements a thread in registers, the next row loaded
+//                        while the current one is reduced
 //
 // Statistics: each thread takes the mean and the centred square sum of its own
 // elements, and (count, mean, M2) are merged by Chan's update, so a large
@@ -342,15 +340,13 @@ struct Ring {
   }
 };
 
-// ROWS rows at a time: their reductions overlap, and a reduction's instructions
-// are shared by 16 elements a thread.  8192 x 7168 bf16: forward 54 us (4.4
-// TB/s, 0.66 of the measured copy), backward 84 us with the column sums (4.2
-// TB/s); what is left is instruction issue and the wait for a row's reduction.
-// Measured and not taken: 8 elements a thread and one row at a time, a CTA of
-// 896 threads (72 and 116 us); one row at a time in two CTAs an SM (52 and
-// 100 us); 16-byte copies by every thread (54 and 96 us).
-template <typename T, int PIECES, int ROWS, int S>
-__global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
+// ROWS rows at a time.  kExact: every thread has all its pieces (d = PIECES kT
+// pieces); otherwise a piece that a thread lacks is zeros that count for
+// nothing.  Either way the code between the barriers has no branch but the
+// warp's choice of merge: with one around each piece 8192 x 7168 bf16 took 54
+// us, now 42 (5.5 TB/s; a plain copy of these bytes takes 39 to 42).
+template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) row_kernel(
     const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, float eps,
     int R, int d, T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
   static_assert(S % ROWS == 0 && S > ROWS, "whole iterations in the ring");
@@ -370,7 +366,7 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
     const int c = (i * kT + t) * V;
 #pragma unroll
     for (int e = 0; e < P; ++e) wv[i][e] = bv[i][e] = 0ull;
-    if (c < d) {
+    if (kExact || c < d) {
       load_f32(w + c, wv[i]);
       if (b != nullptr) load_f32(b + c, bv[i]);
     }
@@ -378,6 +374,11 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
   const float inv_d = 1.f / (float)d;
   // all lanes of the warp hold PIECES whole pieces
   const bool whole = ((PIECES - 1) * kT + (warp + 1) * 32) * V <= d;
+  float warp_n = 0.f;  // this warp's elements
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
+    warp_n += (float)V * __popc(__ballot_sync(0xffffffffu, in.in[i]));
+  const float inv_warp = warp_n > 0.f ? 1.f / warp_n : 0.f;
   int flip = 0;
   size_t row = blockIdx.x;
   for (int done = 0; done < rows; done += ROWS, flip ^= 1) {
@@ -388,33 +389,35 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
     for (int k = 0; k < ROWS; ++k) {
       s[k] = Stat{0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i)
-        if (in.in[i]) {
-          unpack(in.read(k, 0, i), v[k][i], T{});
-          f32x2 sum = v[k][i][0];
+      for (int i = 0; i < PIECES; ++i) {
+        uint4 raw = in.read(k, 0, i);
+        const bool has = kExact || in.in[i];
+        if (!has) raw = make_uint4(0u, 0u, 0u, 0u);
+        unpack(raw, v[k][i], T{});
+        f32x2 sum = v[k][i][0];
 #pragma unroll
-          for (int e = 1; e < P; ++e) sum = add2(sum, v[k][i][e]);
-          const float m = both(sum) * (1.f / V);
-          const f32x2 m1 = pair2(-m, -m);
-          f32x2 sq = 0ull;
+        for (int e = 1; e < P; ++e) sum = add2(sum, v[k][i][e]);
+        const float m = both(sum) * (1.f / V);
+        const f32x2 m1 = pair2(-m, -m);
+        f32x2 sq = 0ull;
 #pragma unroll
-          for (int e = 0; e < P; ++e) {
-            const f32x2 c = add2(v[k][i][e], m1);
-            sq = fma2(c, c, sq);
-          }
-          const float m2 = both(sq);
-          if (i == 0) {
-            s[k] = Stat{(float)V, m, m2};
-          } else {  // equal counts so far: i pieces and one more
-            const float dm = m - s[k].mean;
-            s[k].mean = fmaf(dm, 1.f / (i + 1), s[k].mean);
-            s[k].m2 = fmaf(dm * dm, V * (float)i / (i + 1), s[k].m2 + m2);
-            s[k].n += V;
-          }
+        for (int e = 0; e < P; ++e) {
+          const f32x2 c = add2(v[k][i][e], m1);
+          sq = fma2(c, c, sq);
         }
+        const float m2 = both(sq);
+        if (i == 0) {
+          s[k] = Stat{has ? (float)V : 0.f, m, m2};
+        } else {  // equal counts so far: i pieces and one more, or none
+          const float dm = m - s[k].mean;
+          s[k].mean = fmaf(dm, has ? 1.f / (i + 1) : 0.f, s[k].mean);
+          s[k].m2 = fmaf(dm * dm, has ? V * (float)i / (i + 1) : 0.f, s[k].m2 + m2);
+          s[k].n += has ? (float)V : 0.f;
+        }
+      }
     }
     in.next();
-    if (whole) {  // equal counts: the merged mean is the middle of the two
+    if (kExact || whole) {  // equal counts: the merged mean is the middle of the two
       float n = PIECES * V;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1, n *= 2.f)
@@ -429,7 +432,17 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
         }
     } else {
 #pragma unroll
-      for (int k = 0; k < ROWS; ++k) s[k] = warp_merge(s[k]);
+      for (int k = 0; k < ROWS; ++k) {  // the warp's mean, then the squares around it
+        float a = s[k].n * s[k].mean;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        a *= inv_warp;
+        const float dm = s[k].mean - a;
+        float q = fmaf(s[k].n * dm, dm, s[k].m2);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+        s[k] = Stat{warp_n, a, q};
+      }
     }
     if (lane == 0)
 #pragma unroll
@@ -479,22 +492,22 @@ __global__ void __launch_bounds__(ROWS == 2 ? 512 : 1024) row_kernel(
       row += gridDim.x;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int c = (i * kT + t) * V;
-        if (c < d) {
 #pragma unroll
-          for (int e = 0; e < P; ++e)
-            v[k][i][e] = fma2(mul2(add2(v[k][i][e], mu2), rs2), wv[i][e], bv[i][e]);
-          *reinterpret_cast<uint4*>(dst + c) = pack(v[k][i], T{});
-        }
+        for (int e = 0; e < P; ++e)
+          v[k][i][e] = fma2(mul2(add2(v[k][i][e], mu2), rs2), wv[i][e], bv[i][e]);
+        const uint4 o = pack(v[k][i], T{});
+        if (kExact || in.in[i]) *reinterpret_cast<uint4*>(dst + (i * kT + t) * V) = o;
       }
     }
   }
 }
 
-// One partial row of dw and db per CTA, as below.  kExact: every thread has all
-// its pieces (d = 2 kT pieces), so nothing is predicated.
-template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact>
-__global__ void __launch_bounds__(kThreads) row_bwd_kernel(
+// One partial row of dw and db per CTA, as below.  z and h are kept in registers
+// until the row's sums are known, or (kReread) formed again from the ring, which
+// leaves room for four pieces a thread and two CTAs an SM: 8192 x 7168 bf16 84
+// us kept, 70 reread with the column sums (5.0 TB/s).
+template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact, bool kReread>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) row_bwd_kernel(
     const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ mean, const float* __restrict__ rstd, int R, int d,
     T* __restrict__ dx, float* __restrict__ part) {
@@ -543,7 +556,8 @@ __global__ void __launch_bounds__(kThreads) row_bwd_kernel(
     if (!in.wait())
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) mu[k] = __int_as_float(0x7fffffff);
-    f32x2 z[ROWS][PIECES][P], h[ROWS][PIECES][P];
+    constexpr int KR = kReread ? 1 : ROWS, KP = kReread ? 1 : PIECES;
+    f32x2 z[KR][KP][P], h[KR][KP][P];
     float sums[2 * ROWS];  // h of each row, then h z of each row
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -551,30 +565,35 @@ __global__ void __launch_bounds__(kThreads) row_bwd_kernel(
       if (done + k < rows) {
         const f32x2 mu2 = pair2(-mu[k], -mu[k]), rs2 = pair2(rs[k], rs[k]);
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-          if (kExact || in.in[i]) {
-            f32x2 g[P];
-            unpack(in.read(k, 0, i), z[k][i], T{});
-            unpack(in.read(k, 1, i), g, T{});
+        for (int i = 0; i < PIECES; ++i) {
+          f32x2 g[P];
+          f32x2 (&zi)[P] = z[kReread ? 0 : k][kReread ? 0 : i];
+          f32x2 (&hi)[P] = h[kReread ? 0 : k][kReread ? 0 : i];
+          const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 rx = in.read(k, 0, i), rg = in.read(k, 1, i);
+          const bool has = kExact || in.in[i];
+          unpack(has ? rx : none, zi, T{});
+          unpack(has ? rg : none, g, T{});
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-              z[k][i][e] = mul2(add2(z[k][i][e], mu2), rs2);
-              h[k][i][e] = mul2(g[e], wv[i][e]);
-              s1 = add2(s1, h[k][i][e]);
-              s2 = fma2(h[k][i][e], z[k][i][e], s2);
-              aw[i][e] = fma2(g[e], z[k][i][e], aw[i][e]);
-              ab[i][e] = add2(ab[i][e], g[e]);
-            }
+          for (int e = 0; e < P; ++e) {
+            zi[e] = mul2(add2(zi[e], mu2), rs2);
+            hi[e] = mul2(g[e], wv[i][e]);
+            s1 = add2(s1, hi[e]);
+            s2 = fma2(hi[e], zi[e], s2);
+            aw[i][e] = fma2(g[e], zi[e], aw[i][e]);
+            ab[i][e] = add2(ab[i][e], g[e]);
           }
+        }
       }
       sums[k] = both(s1);
       sums[ROWS + k] = both(s2);
     }
-    in.next();
+    if constexpr (!kReread) in.next();
     const float mine = warp_sums<2 * ROWS>(sums);
     if (lane % (16 / ROWS) == 0) red[flip][lane / (16 / ROWS)][warp] = mine;
     __syncthreads();
-    if (t == 0) in.fetch();  // every thread has read these rows' slots
+    // every thread has read these rows' slots (kReread: those of the rows before)
+    if (t == 0 && (!kReread || done > 0)) in.fetch();
     block_sums<2 * ROWS>(red[flip], warps, sums);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -583,15 +602,28 @@ __global__ void __launch_bounds__(kThreads) row_bwd_kernel(
       const float a = -rs[k] * (sums[k] * inv_d), c = -rs[k] * (sums[ROWS + k] * inv_d);
       const f32x2 rs2 = pair2(rs[k], rs[k]), a2 = pair2(a, a), c2 = pair2(c, c);
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i)
-        if (kExact || in.in[i]) {
+      for (int i = 0; i < PIECES; ++i) {
+        f32x2 o[P];
+        if constexpr (kReread) {
+          f32x2 g[P];
+          const f32x2 mu2 = pair2(-mu[k], -mu[k]);
+          unpack(in.read(k, 0, i), o, T{});
+          unpack(in.read(k, 1, i), g, T{});
 #pragma unroll
-          for (int e = 0; e < P; ++e)
-            z[k][i][e] = fma2(h[k][i][e], rs2, fma2(z[k][i][e], c2, a2));
-          *reinterpret_cast<uint4*>(dst + i * kT * 16) = pack(z[k][i], T{});
+          for (int e = 0; e < P; ++e) {
+            o[e] = mul2(add2(o[e], mu2), rs2);
+            o[e] = fma2(mul2(g[e], wv[i][e]), rs2, fma2(o[e], c2, a2));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) o[e] = fma2(h[k][i][e], rs2, fma2(z[k][i][e], c2, a2));
         }
+        const uint4 u = pack(o, T{});
+        if (kExact || in.in[i]) *reinterpret_cast<uint4*>(dst + i * kT * 16) = u;
+      }
       dst += in.row_step * sizeof(T);
     }
+    if constexpr (kReread) in.next();
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       mu[k] = mu1[k];
@@ -784,32 +816,30 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
   }
 }
 
-// The row kernels take rows of whole 16-byte pieces, two pieces a thread.  Up to
-// 16 KB a row: two rows at a time, a ring of six; up to 32 KB: one at a time, a
-// ring of three (what fits in shared memory).  Narrower than `from` columns a
-// warp per row holds its elements in registers: forward 512 (100000 x 320 bf16
-// 60 us against 70, 30000 x 512 21 against 17), backward 257 (100000 x 320 113
-// us against 80, 16384 x 1024 38 against 34).
-constexpr int kFwdFrom = 512, kBwdFrom = 257;
-bool by_rows(int d, int elem, int from) {
-  return d >= from && d % (16 / elem) == 0 && d * elem <= 32768;
+bool by_rows(int d, int elem) { return d % (16 / elem) == 0 && d * elem <= 32768; }
+// Threads of a row kernel's CTA, and the CTAs an SM holds: 512 threads in all.
+int row_threads(int d, int elem, int pieces) {
+  return ((d / (16 / elem) + pieces - 1) / pieces + 31) / 32 * 32;
 }
-int row_threads(int d, int elem) { return ((d / (16 / elem) + 1) / 2 + 31) / 32 * 32; }
-int rows_per_sm(int d, int elem) {  // CTAs of a row kernel on an SM: 512 threads in all
-  const int t = row_threads(d, elem);
-  return t >= 512 ? 1 : 512 / t;
+int rows_per_sm(int d, int elem, int pieces) {
+  return 512 / row_threads(d, elem, pieces);
 }
+// Pieces a thread.  Forward: two and two rows at a time up to 4096 columns, above
+// four and one row (29 M elements of bf16 in rows of 4096: 41.5 us against 44.5,
+// of 5120: 51.2 against 44.8).  Backward: the same by size, up to 8 KB a row
+// (8192 rows of 2048 bf16 38 us against 50; of 7168 79 against 70).
+int fwd_pieces(int d) { return d <= 4096 ? 2 : 4; }
+int bwd_pieces(int d, int elem) { return d * elem <= 8192 ? 2 : 4; }
 // CTAs of the backward kernel = partial rows.
 int bwd_ctas(int R, int d, int elem) {
-  const bool rows = by_rows(d, elem, kBwdFrom);
+  const bool rows = by_rows(d, elem);
   const int groups = !rows && d <= 1024 ? 4 : 1;
   const long long want = ((long long)R + groups - 1) / groups;
-  const long long most = 148LL * (rows ? rows_per_sm(d, elem) : 2);
+  const long long most = 148LL * (rows ? rows_per_sm(d, elem, bwd_pieces(d, elem)) : 2);
   return (int)(want < most ? (want < 1 ? 1 : want) : most);
 }
 
 struct Fwd {
-  static constexpr int kFrom = kFwdFrom;
   const void* x;
   const float *w, *b;
   float eps;
@@ -818,7 +848,6 @@ struct Fwd {
   float *mean, *rstd;
 };
 struct Bwd {
-  static constexpr int kFrom = kBwdFrom;
   const void *dy, *x;
   const float *w, *mean, *rstd;
   int R, d;
@@ -843,85 +872,76 @@ void go(const Bwd& a, cudaStream_t st) {
       static_cast<T*>(a.dx), a.part);
 }
 
-template <typename T, int ROWS, int S>
+template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact>
 cudaError_t rows_launch(const Fwd& a, cudaStream_t st) {
-  const int kT = row_threads(a.d, sizeof(T));
-  const size_t smem = (size_t)S * 2 * kT * 16;
-  auto kernel = row_kernel<T, 2, ROWS, S>;
+  const int kT = row_threads(a.d, sizeof(T), PIECES);
+  auto kernel = row_kernel<T, PIECES, ROWS, S, kThreads, kExact>;
   // the same opt-in for every width: host threads may call at the same time
-  constexpr int most_smem = S * 2 * (ROWS == 2 ? 512 : 1024) * 16;
+  constexpr int most_smem = S * PIECES * kThreads * 16;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        most_smem);
   if (e != cudaSuccess) return e;
-  const int most = 148 * rows_per_sm(a.d, sizeof(T));
-  kernel<<<a.R < most ? a.R : most, kT, smem, st>>>(static_cast<const T*>(a.x), a.w, a.b, a.eps,
-                                                    a.R, a.d, static_cast<T*>(a.y), a.mean,
-                                                    a.rstd);
+  const int most = 148 * rows_per_sm(a.d, sizeof(T), PIECES);
+  kernel<<<a.R < most ? a.R : most, kT, S * PIECES * kT * 16, st>>>(
+      static_cast<const T*>(a.x), a.w, a.b, a.eps, a.R, a.d, static_cast<T*>(a.y), a.mean, a.rstd);
   return cudaGetLastError();
 }
-template <typename T, int ROWS, int S, int kThreads, bool kExact>
-cudaError_t rows_launch_bwd(const Bwd& a, cudaStream_t st) {
-  const int kT = row_threads(a.d, sizeof(T));
-  const size_t smem = (size_t)S * 2 * 2 * kT * 16;
-  auto kernel = row_bwd_kernel<T, 2, ROWS, S, kThreads, kExact>;
-  constexpr int most_smem = S * 2 * 2 * kThreads * 16;
+template <typename T, int PIECES, int ROWS, int S, int kThreads, bool kExact>
+cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
+  const int kT = row_threads(a.d, sizeof(T), PIECES);
+  auto kernel = row_bwd_kernel<T, PIECES, ROWS, S, kThreads, kExact, ROWS == 1>;
+  constexpr int most_smem = S * PIECES * 2 * kThreads * 16;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        most_smem);
   if (e != cudaSuccess) return e;
-  kernel<<<bwd_ctas(a.R, a.d, sizeof(T)), kT, smem, st>>>(
+  kernel<<<bwd_ctas(a.R, a.d, sizeof(T)), kT, S * PIECES * 2 * kT * 16, st>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.mean, a.rstd, a.R, a.d,
       static_cast<T*>(a.dx), a.part);
   return cudaGetLastError();
 }
-template <typename T, int ROWS, int S>
-cudaError_t rows_launch(const Bwd& a, cudaStream_t st) {
-  const int kT = row_threads(a.d, sizeof(T));
-  const bool exact = a.d == 2 * kT * (16 / (int)sizeof(T));
-  if constexpr (ROWS == 2) {
-    // up to 448 threads a thread may have 144 registers instead of 128
-    if (kT <= 448)
-      return exact ? rows_launch_bwd<T, ROWS, S, 448, true>(a, st)
-                   : rows_launch_bwd<T, ROWS, S, 448, false>(a, st);
-    return rows_launch_bwd<T, ROWS, S, 512, false>(a, st);
-  } else {
-    return rows_launch_bwd<T, ROWS, S, 1024, false>(a, st);
-  }
+template <typename T, int PIECES, int ROWS, int S, int kThreads, typename Args>
+cudaError_t rows_full(const Args& a, cudaStream_t st) {
+  if (a.d == PIECES * row_threads(a.d, sizeof(T), PIECES) * (16 / (int)sizeof(T)))
+    return rows_launch<T, PIECES, ROWS, S, kThreads, true>(a, st);
+  return rows_launch<T, PIECES, ROWS, S, kThreads, false>(a, st);
 }
-template <typename T, typename Args>
-cudaError_t rows(const Args& a, cudaStream_t st) {
-  if (a.d * (int)sizeof(T) <= 16384) return rows_launch<T, 2, 6>(a, st);
-  return rows_launch<T, 1, 3>(a, st);
+template <typename T>
+cudaError_t rows(const Fwd& a, cudaStream_t st) {
+  if (fwd_pieces(a.d) == 2) return rows_full<T, 2, 2, 6, 128 * sizeof(T)>(a, st);
+  if (a.d * (int)sizeof(T) <= 16384) return rows_full<T, 4, 1, 6, 256>(a, st);
+  return rows_full<T, 4, 1, 6, 512>(a, st);
+}
+template <typename T>
+cudaError_t rows(const Bwd& a, cudaStream_t st) {
+  if (bwd_pieces(a.d, sizeof(T)) == 2) return rows_full<T, 2, 2, 6, 256>(a, st);
+  if (a.d * (int)sizeof(T) <= 16384) return rows_full<T, 4, 1, 3, 256>(a, st);
+  return rows_full<T, 4, 1, 3, 512>(a, st);
 }
 
-// Elements in registers: as few threads per row as hold it in 32 elements each,
-// fewer elements for short rows.  Aligned rows come here where they are narrow,
-// or (fp32) wider than the row kernels take.
-template <typename T, int VEC, typename Args>
+// Elements in registers, 8 to 32 a thread: rows that are not whole 16-byte
+// pieces, and fp32 rows wider than the row kernels take.
+template <typename T, typename Args>
 void by_width(const Args& a, cudaStream_t st) {
-  if (a.d <= 256) return go<T, VEC, 8 / VEC, 32>(a, st);
-  if constexpr (VEC == 1 || Args::kFrom > 257) {
-    if (a.d <= 512) return go<T, VEC, 16 / VEC, 32>(a, st);
+  if (a.d <= 256) return go<T, 1, 8, 32>(a, st);
+  if (a.d <= 512) return go<T, 1, 16, 32>(a, st);
+  if (a.d <= 1024) return go<T, 1, 32, 32>(a, st);
+  if (a.d <= 2048) return go<T, 1, 16, 128>(a, st);
+  if (a.d <= 4096) return go<T, 1, 32, 128>(a, st);
+  if (a.d <= 8192) return go<T, 1, 32, 256>(a, st);
+  if constexpr (sizeof(T) == 4) {
+    if (a.d % 4 == 0) return go<T, 4, 8, 512>(a, st);
   }
-  if constexpr (VEC == 1) {
-    if (a.d <= 1024) return go<T, VEC, 32, 32>(a, st);
-    if (a.d <= 2048) return go<T, VEC, 16, 128>(a, st);
-    if (a.d <= 4096) return go<T, VEC, 32, 128>(a, st);
-    if (a.d <= 8192) return go<T, VEC, 32, 256>(a, st);
-  }
-  if constexpr (VEC == 1 || sizeof(T) == 4) go<T, VEC, 32 / VEC, 512>(a, st);
+  go<T, 1, 32, 512>(a, st);
+}
+template <typename T, typename Args>
+cudaError_t by_type(const Args& a, cudaStream_t st) {
+  if (by_rows(a.d, sizeof(T))) return rows<T>(a, st);
+  by_width<T>(a, st);
+  return cudaGetLastError();
 }
 template <typename Args>
-cudaError_t by_type(const Args& a, int dtype, cudaStream_t st) {
-  if (by_rows(a.d, (int)dtype_bytes(dtype), Args::kFrom))
-    return dtype == MOE_DTYPE_BF16 ? rows<__nv_bfloat16>(a, st) : rows<float>(a, st);
-  if (dtype == MOE_DTYPE_BF16) {
-    if (a.d % 8 == 0) by_width<__nv_bfloat16, 8>(a, st);
-    else by_width<__nv_bfloat16, 1>(a, st);
-  } else {
-    if (a.d % 4 == 0) by_width<float, 4>(a, st);
-    else by_width<float, 1>(a, st);
-  }
-  return cudaGetLastError();
+cudaError_t launch_norm(const Args& a, int dtype, cudaStream_t st) {
+  return dtype == MOE_DTYPE_BF16 ? by_type<__nv_bfloat16>(a, st) : by_type<float>(a, st);
 }
 
 }  // namespace
@@ -935,7 +955,7 @@ size_t layer_norm_ws_bytes(int R, int d) {  // for either type
 
 cudaError_t launch_layer_norm(int dtype, const void* x, const float* w, const float* b, float eps,
                               int R, int d, void* y, float* mean, float* rstd, cudaStream_t st) {
-  return note_cuda(by_type(Fwd{x, w, b, eps, R, d, y, mean, rstd}, dtype, st),
+  return note_cuda(launch_norm(Fwd{x, w, b, eps, R, d, y, mean, rstd}, dtype, st),
                    "layer norm launch");
 }
 
@@ -944,7 +964,7 @@ cudaError_t launch_layer_norm_backward(int dtype, const void* dy, const void* x,
                                        void* dx, float* dw, float* db, void* ws,
                                        cudaStream_t st) {
   float* part = static_cast<float*>(ws);
-  cudaError_t e = note_cuda(by_type(Bwd{dy, x, w, mean, rstd, R, d, dx, part}, dtype, st),
+  cudaError_t e = note_cuda(launch_norm(Bwd{dy, x, w, mean, rstd, R, d, dx, part}, dtype, st),
                             "layer norm backward launch");
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
