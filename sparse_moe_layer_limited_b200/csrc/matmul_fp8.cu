@@ -445,19 +445,20 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inverse) {
 // values per lane (lanes past the last column hold zeros), four tiles at a time:
 // four loads a lane are in flight, and lane j of the half computes tile j's
 // scale for all.  The max-abs is taken on packed bf16 pairs (exact).  The
-// tile's row and block advance by constants; one division at the start.
+// tile's row and block advance by constants; one division at the start.  Four
+// resident CTAs an SM and only the stores predicated: 8192 x 7168 36 us (4.95
+// TB/s; eight CTAs in two waves, with branches around the code making, 42).
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {  // of a (>= 0) and |b|
   b &= 0x7fff7fffu;
   const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
+constexpr int kQuantCtas = 4;
 template <bool kE5M2>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16* __restrict__ x,
-                                                            long long rows, int cols,
-                                                            uint8_t* __restrict__ q,
-                                                            float* __restrict__ sc,
-                                                            long long sc_ld) {
+__global__ void __launch_bounds__(256, kQuantCtas) quantize_rows_kernel(
+    const __nv_bfloat16* __restrict__ x, long long rows, int cols, uint8_t* __restrict__ q,
+    float* __restrict__ sc, long long sc_ld) {
   constexpr int kUnroll = 4;
   const int per_row = (cols + QB - 1) / QB;
   const int l16 = threadIdx.x & 15;
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16*
       const float inverse = __shfl_sync(0xffffffffu, s.inverse, j, 16);
       float v[8];
       bf16x8_to_f32(raw[j], v);
-      if (at[j] >= 0) *reinterpret_cast<uint2*>(q + at[j]) = codes8<kE5M2>(v, inverse);
+      const uint2 codes = codes8<kE5M2>(v, inverse);
+      if (at[j] >= 0) *reinterpret_cast<uint2*>(q + at[j]) = codes;
     }
   }
 }
@@ -614,7 +616,7 @@ cudaError_t launch_quantize_rows_fp8(const void* x, long long rows, int cols, in
                                      cudaStream_t st) {
   const long long tiles = rows * ((cols + QB - 1) / QB);
   long long blocks = (tiles * 16 + 255) / 256;
-  if (blocks > 148 * 8) blocks = 148 * 8;
+  if (blocks > 148 * kQuantCtas) blocks = 148 * kQuantCtas;
   auto kernel = e5m2 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>;
   kernel<<<(int)blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, codes,
                                       scales, sc_ld);
