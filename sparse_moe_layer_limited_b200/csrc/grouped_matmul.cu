@@ -36,8 +36,8 @@
 // with one elected lane issuing: from one lane of a diverged branch the same
 // kernel was 12-18% slower.
 //
-// Units are ordered expert-major, then M tile, then N tile: pairs running side
-// by side share weights and rows through L2, and each expert's weights stream
+// Units are ordered expert-major, then in blocks of N tiles (raster below): pairs
+// running side by side share weights and rows through L2, and each expert's weights stream
 // from HBM once.  Rows of the next expert inside a load only reach output rows
 // that are not stored.  The weight gradient contracts over the rows: in an
 // expert's last K block the rows past its end are overwritten with zeros in
@@ -620,6 +620,8 @@ int launch_grouped_matmul_bf16(int mode, const void* rows, int R, const int32_t*
 
 int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const int32_t* offsets,
                                   int E, int n, int k, void* dw, void* ws, cudaStream_t st) {
+  if (matmul_dw_splits(R, E, n, k) > 1)
+    return launch_matmul_dw_small(dy, x, R, offsets, E, n, k, dw, ws, st);
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   GArgs a{};
   a.offsets = offsets;

@@ -210,6 +210,11 @@ int launch_grouped_matmul_dw_bf16(const void* dy, const void* x, int R, const in
 int launch_grouped_matmul_fp32(int mode, const float* a, const float* b, int R,
                                const int32_t* offsets, int E, int n, int k, float* out, void* ws,
                                cudaStream_t st);
+// Weight gradients of few output tiles and many rows (matmul_dw_small.cu): CTAs
+// that share a tile; 1: not a case for that kernel.
+int matmul_dw_splits(int R, int E, int n, int k);
+int launch_matmul_dw_small(const void* dy, const void* x, int R, const int32_t* offsets, int E,
+                           int n, int k, void* dw, void* ws, cudaStream_t st);
 // Few rows (matmul_narrow.cu): whether a call of R rows, E experts and `cols`
 // output columns runs there, and the launch (a_scales NULL: bf16).
 bool matmul_is_narrow(int R, int E, int cols);

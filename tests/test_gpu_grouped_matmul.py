@@ -127,6 +127,42 @@ def test_weight_gradient(M, ws, dtype, counts, lead, behind, n, k):
     close(dw, want, mag, max(counts))
 
 
+# few output tiles and many rows (their contraction is split over clusters), and
+# tiles enough for the others
+@pytest.mark.parametrize("counts,lead,behind,n,k", [
+    ([5001], 0, 0, 8, 8), ([600], 1, 3, 136, 264), ([1500, 0, 37, 2103], 3, 5, 72, 40),
+    ([0, 0, 4500], 0, 9, 264, 136), ([9000, 1], 2, 0, 128, 1032), ([64 * 40 + 1], 5, 70, 40, 2056),
+    ([777] * 5, 0, 0, 128, 128), ([129, 0, 1000, 33], 7, 2, 1032, 1160)])
+def test_weight_gradient_of_many_rows(M, ws, counts, lead, behind, n, k):
+    g = gen(23)
+    R = lead + sum(counts) + behind
+    dy, x = rand(g, R, n, dtype=BF), rand(g, R, k, dtype=BF)
+    for t in (dy, x):
+        t[:lead] = float("nan")
+        t[R - behind:R] = float("nan")
+    dw = torch.full((len(counts), n, k), 7.0, dtype=BF, device="cuda")
+    M.moe_grouped_matmul_dw(dy, x, offsets_of(counts, lead), dw, ws)
+    close(dw, *expected("dw", dy, x, counts, lead, n, k), max(counts))
+    again = torch.empty_like(dw)
+    for _ in range(3):
+        M.moe_grouped_matmul_dw(dy, x, offsets_of(counts, lead), again, ws)
+        assert torch.equal(again, dw)
+
+
+def test_split_weight_gradients_and_bad_offsets(M):
+    """The other experts' gradients stay right; the bad one's are zeros."""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    g = gen(24)
+    dy, x = rand(g, 3000, 40, dtype=BF), rand(g, 3000, 72, dtype=BF)
+    off = torch.tensor([0, 1400, 1200, 3000], dtype=torch.int32, device="cuda")
+    dw = torch.full((3, 40, 72), 7.0, dtype=BF, device="cuda")
+    M.moe_grouped_matmul_dw(dy, x, off, dw, ws)
+    assert (dw[1] == 0).all() and M.moe_read_device_status(ws) != 0
+    for e, s in ((0, slice(0, 1400)), (2, slice(1200, 3000))):
+        a, b = dy[s].double(), x[s].double()
+        close(dw[e], a.t() @ b, a.abs().t() @ b.abs(), 1800)
+
+
 def test_fp32_takes_any_width(M, ws):
     g = gen(3)
     counts, n, k = [3, 0, 66, 130], 37, 101
