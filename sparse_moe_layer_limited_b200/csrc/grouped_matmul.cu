@@ -25,7 +25,10 @@
 // moves 64 KB for 512 cycles of MMA, near what L2 gives 148 SMs at once, and a
 // tile of 144 rows moves 50 KB for 288.  So with enough units two row tiles of
 // an expert share one unit: each W block is staged once for both, and both
-// accumulators (256 TMEM columns each) are filled.
+// accumulators (256 TMEM columns each) are filled.  Where the last round would
+// leave most pairs idle its experts' units are cut in two again (ragged_schedule;
+// forward of 32 x 512 rows, 2048 x 4096: 343 -> 322 us, of 64 x about 400 rows,
+// 1536 x 2048: 197 -> 183).
 //
 // Measured, bf16: 8192 x 4096 x 7168 dense forward 318 us in a burst (1.51
 // PFLOP/s), 369 us under sustained power, level with the library's product of
@@ -157,6 +160,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
   uint64_t* tland = reinterpret_cast<uint64_t*>(tmem_holder) + 1;
   uint64_t* tclear = tland + kStages;
   int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  int* single = start - 1;  // fwd, dx: from this expert on a unit is one row tile
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -188,8 +192,11 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
     tmem_relinquish_2sm();
   }
   if constexpr (kMode != kDw) {
-    if (warp == 0)
-      ragged_schedule(args.offsets, args.E, args.R, kShare * GN, MT, start, args.status);
+    if (warp == 0) {
+      const int from = ragged_schedule(args.offsets, args.E, args.R, kShare * GN, MT, start,
+                                       args.status, kShare == 2 ? npairs : 0);
+      if (lane == 0) *single = from;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -225,14 +232,15 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       t.g = ragged_group(start, args.E, u);
       t.rows = group_rows(args.offsets, t.g, args.R, &t.first, &bad);
       const int tiles = (t.rows + GN - 1) / GN, local = u - start[t.g];
-      const int runs = (tiles + kShare - 1) / kShare;  // units per M tile
+      const int each = kShare == 2 && t.g < *single ? 2 : 1;  // row tiles per unit
+      const int runs = (tiles + each - 1) / each;  // units per M tile
       int m, n;
       raster(local, MT, runs, m, n);
-      const int w = row_tile(t.rows, tiles), t0 = n * kShare;
+      const int w = row_tile(t.rows, tiles), t0 = n * each;
       t.m0 = m * GM;
       t.n0 = t0 * w;
       t.width[0] = min(w, (t.rows - t.n0 + 31) & ~31);
-      if (kShare == 2 && t0 + 1 < tiles) {
+      if (each == 2 && t0 + 1 < tiles) {
         t.tiles = 2;
         t.width[1] = min(w, (t.rows - t.n0 - w + 31) & ~31);
       }

@@ -83,34 +83,56 @@ __device__ __forceinline__ int group_rows(const int32_t* offsets, int g, int R, 
   return hi - lo;
 }
 
-// start[g] = units before group g when each group has ceil(rows / tile_m) * per
-// units; start[E] = their total.  Called by one warp.
-__device__ __forceinline__ void ragged_schedule(const int32_t* offsets, int E, int R, int tile_m,
-                                                int per, int* start, uint32_t* status) {
+// start[g] = units before group g, start[E] = their total; called by one warp.  A
+// group of `rows` rows has ceil(rows / tile_m) runs of `per` units.  `pairs` > 0:
+// that many workers take the units in turn, and a unit may be cut in two (runs of
+// tile_m / 2 rows).  Where the last round leaves more than half of the workers
+// without a unit, the groups that reach into it are cut, if the halves then fit
+// into half a round: with `rest` units in the last round, and the first of these
+// groups starting s units before it, 2 rest + s halves.  Returns the first group
+// that is cut (E: none).
+__device__ __forceinline__ int ragged_schedule(const int32_t* offsets, int E, int R, int tile_m,
+                                               int per, int* start, uint32_t* status,
+                                               int pairs = 0) {
   const int lane = threadIdx.x & 31;
   const int chunk = (E + 31) / 32;
   const int g0 = min(E, lane * chunk), g1 = min(E, g0 + chunk);
   bool bad = false;
-  int first, sum = 0;
-  for (int g = g0; g < g1; ++g) {
-    const int mt = (group_rows(offsets, g, R, &first, &bad) + tile_m - 1) / tile_m;
-    start[g] = mt;
-    sum += mt;
-  }
-  int inc = sum;
+  int first, single = E;
+  for (int pass = 0; pass < 2; ++pass) {
+    int sum = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int tm = g < single ? tile_m : tile_m / 2;
+      const int mt = (group_rows(offsets, g, R, &first, &bad) + tm - 1) / tm;
+      start[g] = mt;
+      sum += mt;
+    }
+    int inc = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    int run = inc - sum;
+    const int total = __shfl_sync(0xffffffffu, inc, 31) * per;
+    const int rest = pairs > 0 ? total % pairs : 0;
+    const int round = total - rest;  // units before the last round
+    int from = E;
+    for (int g = g0; g < g1; ++g) {
+      const int before = run * per;
+      run += start[g];
+      start[g] = before;
+      if (rest > 0 && before <= round && run * per > round && 2 * rest + round - before <= pairs)
+        from = g;
+    }
+    if (lane == 31) start[E] = total;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) from = min(from, __shfl_xor_sync(0xffffffffu, from, o));
+    if (pass == 1 || from == E) break;
+    single = from;
   }
-  int run = inc - sum;
-  for (int g = g0; g < g1; ++g) {
-    const int mt = start[g];
-    start[g] = run * per;
-    run += mt;
-  }
-  if (lane == 31) start[E] = inc * per;
   if (bad) atomicOr(status, kErrBadIndex);
+  return single;
 }
 
 // The group of unit u: start[g] <= u < start[g + 1].

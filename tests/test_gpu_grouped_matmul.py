@@ -163,6 +163,23 @@ def test_split_weight_gradients_and_bad_offsets(M):
         close(dw[e], a.t() @ b, a.abs().t() @ b.abs(), 1800)
 
 
+@pytest.mark.parametrize("mode", ["fwd", "dx"])
+@pytest.mark.parametrize("counts,m", [
+    ([512] * 32, 2048),                                   # 222 units of two tiles, 34 in the last
+    ([257 + 8 * e for e in range(31)] + [0, 3], 2048),    # round: the last experts' are cut
+    ([511, 1, 0, 700, 260] * 8 + [300], 1288), ([8190], 5000)])
+def test_units_cut_in_the_last_round(M, ws, mode, counts, m):
+    g = gen(25)
+    n, k = (m, 72) if mode == "fwd" else (72, m)
+    R, off = sum(counts) + 2, offsets_of(counts, 1)
+    a, w = rand(g, R, 72, dtype=BF), rand(g, len(counts), n, k, dtype=BF)
+    out = torch.full((R, m), 7.0, dtype=BF, device="cuda")
+    (M.moe_grouped_matmul if mode == "fwd" else M.moe_grouped_matmul_dx)(a, off, w, out, ws)
+    want, mag = expected(mode, a, w, counts, 1, n, k)
+    close(out[1:-1], want[1:-1], mag[1:-1], 72)
+    assert (out[0] == 7.0).all() and (out[-1] == 7.0).all()
+
+
 def test_fp32_takes_any_width(M, ws):
     g = gen(3)
     counts, n, k = [3, 0, 66, 130], 37, 101
