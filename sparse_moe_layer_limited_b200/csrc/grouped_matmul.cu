@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       }
       t = next;
     }
-    if (!ok) {  // let the copies already issued land before the CTA exits
-      for (int s = 0; s < kStages; ++s) {
-        if (leader && ((issued >> s) & 1u))
-          mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
-        if (kMode == kDw && ((tissued >> s) & 1u))
-          mm_wait(&tland[s], ((tphase >> s) & 1u) ^ 1u, args.status, kMatmulTimeoutNs / 8);
-      }
+    // every copy has landed before the CTA exits, also where the warp that reads
+    // them gave up; the leader's barriers count the peer's copies too
+    for (int s = 0; s < kStages; ++s) {
+      if (leader && ((issued >> s) & 1u)) mm_drain(&full[s], (parity >> s) & 1u, args.status);
+      if (kMode == kDw && ((tissued >> s) & 1u))
+        mm_drain(&tland[s], ((tphase >> s) & 1u) ^ 1u, args.status);
     }
+    mm_settle(args.status);
   } else if (warp == 1) {
     if (leader) {
       // ---- MMA issuer: the warp walks the loop together, so that addresses stay
@@ -427,11 +427,9 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
         use += t.tiles;
         t = next;
       }
-      if (elect_one()) {
-        mma_commit_2sm(drain);
-        mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
-      }
+      if (elect_one()) mma_commit_2sm(drain);
       __syncwarp();
+      mm_drain(drain, 0, args.status);
     } else if (!leader && lane == 0) {
       // forward each accumulator release of this CTA's epilogue to the leader
       const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       for (int u = pair; u < total && ok; u += npairs) {
         const Unit t = decode(u);
         for (int j = 0; j < t.tiles && ok; ++j, ++use) {
-          ok = mm_wait(&edone[use & 1], (use >> 1) & 1, args.status);
+          ok = mm_wait_thread(&edone[use & 1], (use >> 1) & 1, args.status);
           if (ok) mbar_arrive_peer(tempty0 + 8u * (uint32_t)(use & 1));
         }
       }

@@ -155,13 +155,14 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
           phase ^= 1u;
         }
       }
+      if (u + step >= total) {
+        // every copy has landed before the CTA exits, also where the MMA warp gave up
+        // (before the last barriers: here the wait is under the products')
+        for (int s = 0; s < DStages; ++s)
+          if ((issued >> s) & 1u) mm_drain(&full[s], (parity >> s) & 1u, args.status);
+      }
       cluster_sync_all();
       cluster_sync_all();
-    }
-    if (!ok) {  // let the copies already issued land before the CTA exits
-      for (int s = 0; s < DStages; ++s)
-        if ((issued >> s) & 1u)
-          mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
     }
   } else if (warp == 1) {
     // ---- MMA issuer ----
@@ -215,11 +216,9 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
       cluster_sync_all();
       cluster_sync_all();
     }
-    if (elect_one()) {
-      mma_commit(drain);
-      mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
-    }
+    if (elect_one()) mma_commit(drain);
     __syncwarp();
+    mm_drain(drain, 0, args.status);
   } else {
     // ---- epilogue: a TMEM lane is a row of the tile ----
     const int q = warp & 3, row = q * 32 + lane, et = tid - 64;

@@ -199,11 +199,9 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
         }
         t = next;
       }
-      if (!ok) {
-        for (int s = 0; s < PStages; ++s)
-          if ((issued >> s) & 1u)
-            mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
-      }
+      // every copy has landed before the CTA exits, also where the MMA warp gave up
+      for (int s = 0; s < PStages; ++s)
+        if ((issued >> s) & 1u) mm_drain(&full[s], (parity >> s) & 1u, args.status);
     } else if (warp == 1) {
       // ---- MMA issuer, one TMEM buffer per slice ----
       const uint32_t ring = smem_u32(base);
@@ -247,11 +245,9 @@ __global__ void __launch_bounds__(PThreads, 1) matmul_fp8_kernel(
         }
         t = next;
       }
-      if (elect_one()) {
-        mma_commit(drain);
-        mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
-      }
+      if (elect_one()) mma_commit(drain);
       __syncwarp();
+      mm_drain(drain, 0, args.status);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");

@@ -191,15 +191,16 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
           phase ^= 1u;
         }
       }
+      if (u + step >= total) {
+        // every copy has landed before the CTA exits, also where the MMA warp gave up
+        // (before the last barriers: here the wait is under the products')
+        for (int s = 0; s < NStages; ++s)
+          if ((issued >> s) & 1u) mm_drain(&full[s], (parity >> s) & 1u, args.status);
+      }
       if (S > 1) {
         cluster_sync_all();
         cluster_sync_all();
       }
-    }
-    if (!ok) {  // let the copies already issued land before the CTA exits
-      for (int s = 0; s < NStages; ++s)
-        if ((issued >> s) & 1u)
-          mm_wait(&full[s], (parity >> s) & 1u, args.status, kMatmulTimeoutNs / 8);
     }
   } else if (warp == 1) {
     // ---- MMA issuer ----
@@ -251,11 +252,9 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
         cluster_sync_all();
       }
     }
-    if (elect_one()) {
-      mma_commit(drain);
-      mm_wait(drain, 0, args.status, kMatmulTimeoutNs / 8);
-    }
+    if (elect_one()) mma_commit(drain);
     __syncwarp();
+    mm_drain(drain, 0, args.status);
   } else {
     // ---- epilogue: lane = output column, register = row ----
     const int q = warp & 3;

@@ -9,15 +9,13 @@
 namespace moe {
 
 constexpr int kMatmulMaxGroups = 384;  // tile table entries that fit beside the operand ring
-constexpr uint64_t kMatmulTimeoutNs = 2000000000ull;
+// Waits are timed in steps of 2^20 ns (about a millisecond), in 32 bits.
+constexpr uint32_t kMatmulTimeoutMs = 2000, kDrainMs = 50;
+__device__ __forceinline__ uint32_t clock_ms() { return (uint32_t)(globaltimer_ns() >> 20); }
 
-// mbar_wait_bounded for the matmul kernels: only a recorded time-out makes
-// other waits give up, so a call that reports bad offsets still completes its
-// good groups; and the clock is first read after 64 tries, as reading it on
-// every wait that does not succeed at once delays the pipeline.  kCluster:
-// cluster-scope acquire, for barriers the peer CTA arrives on.
+// One try of a wait.  `cluster`: cluster-scope acquire, for barriers that the
+// peer CTA arrives on.
 __device__ __forceinline__ bool mm_try(uint64_t* bar, uint32_t parity, bool cluster) {
-  constexpr uint32_t kSuspendNs = 20000;  // the warp sleeps up to this long per try
   uint32_t ok;
   if (cluster)
     asm volatile(
@@ -37,18 +35,69 @@ __device__ __forceinline__ bool mm_try(uint64_t* bar, uint32_t parity, bool clus
         : "memory");
   return ok != 0;
 }
+// mbar_wait_bounded for the matmul kernels: only a recorded time-out makes
+// other waits give up, so a call that reports bad offsets still completes its
+// good groups; and the clock is first read after 64 tries, as reading it on
+// every wait that does not succeed at once delays the pipeline.
+//
+// The whole warp waits and gets one verdict: elect.sync, __syncwarp and aligned
+// cluster barriers follow, which lanes that go different ways never leave.  Each
+// lane sees the phase for itself (that orders its later reads); a lane that has
+// seen it keeps seeing it, so the warp gives up only while no lane has, on the
+// word of lane 0.
 template <bool kCluster = false>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                        uint64_t limit_ns = kMatmulTimeoutNs) {
-  auto ready = [&] { return mm_try(bar, parity, kCluster); };
-  uint64_t t0 = 0;
+                                        uint32_t limit_ms = kMatmulTimeoutMs) {
+  uint32_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (ready()) return true;
+    const bool ready = mm_try(bar, parity, kCluster);
+    if (__all_sync(0xffffffffu, ready)) return true;
+    if (it == 64) t0 = clock_ms();
+    if ((it & 63u) == 0 && !__any_sync(0xffffffffu, ready)) {
+      uint32_t seen = *reinterpret_cast<volatile uint32_t*>(err) & kErrWaitTimeout;
+      if (clock_ms() - t0 > limit_ms) {
+        atomicOr(err, kErrWaitTimeout);
+        seen = 1;
+      }
+      if (__shfl_sync(0xffffffffu, seen, 0)) return false;
+    }
+  }
+}
+// The whole warp waits for its own copies or products in flight before the CTA
+// ends, whatever the status word says: a CTA that gives up because another one
+// has must not hand its shared memory on while copies still write to it.
+__device__ __forceinline__ void mm_drain(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  uint32_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mm_try(bar, parity, false))) return;
+    if ((it & 63u) == 0) {
+      if (it == 64) t0 = clock_ms();
+      const bool over = clock_ms() - t0 > kDrainMs;
+      if (over) atomicOr(err, kErrWaitTimeout);
+      if (__shfl_sync(0xffffffffu, over, 0)) return;
+    }
+  }
+}
+// After a recorded time-out: time for copies to land whose barrier may never
+// complete (a pair's peer signals the leader's, which may not have armed it).
+// A copy lands within microseconds.
+__device__ __forceinline__ void mm_settle(const uint32_t* err) {
+  if (*reinterpret_cast<const volatile uint32_t*>(err) & kErrWaitTimeout) {
+    const uint32_t t0 = clock_ms();
+    while (clock_ms() - t0 < 2) __nanosleep(1000);
+  }
+  __syncwarp();
+}
+// mm_wait for a single thread.
+__device__ __forceinline__ bool mm_wait_thread(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               uint32_t limit_ms = kMatmulTimeoutMs) {
+  uint32_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mm_try(bar, parity, false)) return true;
     if ((it & 63u) == 0) {
       if (*reinterpret_cast<volatile uint32_t*>(err) & kErrWaitTimeout) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > limit_ns) {
+      if (it == 64) t0 = clock_ms();
+      if (clock_ms() - t0 > limit_ms) {
         atomicOr(err, kErrWaitTimeout);
         return false;
       }
