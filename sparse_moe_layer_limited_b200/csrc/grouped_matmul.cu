@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers exist before either signals the other
+  mm_cluster_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int total = kMode == kDw ? args.E * MT * NT : start[args.E];
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
               for (int i = 0; i < 32; ++i) p[i] = 0u;
             } else {
               uint32_t v0[32], v1[32];
+              __syncwarp();  // lane 0 has stored the piece before
               tmem_ld32(taddr + c, v0);
               tmem_ld32(taddr + c + 32, v1);
               tmem_wait_ld();
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
             const int left = t.rows - n0 - b;
             if (left <= 0) break;
             uint32_t v[32];
+            __syncwarp();  // lane 0 has stored the block before
             tmem_ld32(taddr + b, v);
             tmem_wait_ld();
             uint8_t* tile = stg + buf * 2048;
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  mm_cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_2sm(tmem_base, kTmemCols);

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(SThreads, BM == 16 ? 4 : 2) grouped_matmul_fp3
           *reinterpret_cast<float4*>(shared + row_of(i) * BN + h * (BN / TN) * CV + tx * CV) =
               make_float4(acc[i][CV * h], acc[i][CV * h + 1], acc[i][CV * h + 2],
                           acc[i][CV * h + 3]);
-      cluster_sync_all();
+      mm_cluster_sync();
       for (int q = rank * SThreads + tid; q < BM * BN / 4; q += S * SThreads) {
         const uint32_t at = smem_u32(shared + 4 * q);
         float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(SThreads, BM == 16 ? 4 : 2) grouped_matmul_fp3
         }
         store(4 * q / BN, 4 * q % BN, v);
       }
-      cluster_sync_all();  // everyone has read this CTA's partial tile
+      mm_cluster_sync();  // everyone has read this CTA's partial tile
     }
   }
 }

@@ -161,8 +161,8 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
         for (int s = 0; s < DStages; ++s)
           if ((issued >> s) & 1u) mm_drain(&full[s], (parity >> s) & 1u, args.status);
       }
-      cluster_sync_all();
-      cluster_sync_all();
+      mm_cluster_sync();
+      mm_cluster_sync();
     }
   } else if (warp == 1) {
     // ---- MMA issuer ----
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
           phase ^= 1u;
         }
       }
-      cluster_sync_all();
-      cluster_sync_all();
+      mm_cluster_sync();
+      mm_cluster_sync();
     }
     if (elect_one()) mma_commit(drain);
     __syncwarp();
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
         __syncwarp();
         if (t.kcnt > 0 && lane == 0) mbar_arrive(&tempty[buf]);
       }
-      cluster_sync_all();
+      mm_cluster_sync();
       // 8 columns a thread, sixteen threads a row
       for (int i = rank * 128 + et; i < DT * (DT / 8); i += S * 128) {
         const int r = i >> 4, c = (i & 15) * 8;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
               make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
                          bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
       }
-      cluster_sync_all();  // everyone has read this CTA's partial tile
+      mm_cluster_sync();  // everyone has read this CTA's partial tile
     }
   }
 

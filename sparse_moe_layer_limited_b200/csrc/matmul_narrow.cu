@@ -83,7 +83,10 @@ __device__ __forceinline__ float peer_f32(uint32_t local, uint32_t rank) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
 
 template <bool kFp8, bool kDx>
 __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
@@ -198,8 +201,8 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
           if ((issued >> s) & 1u) mm_drain(&full[s], (parity >> s) & 1u, args.status);
       }
       if (S > 1) {
-        cluster_sync_all();
-        cluster_sync_all();
+        mm_cluster_sync();
+        mm_cluster_sync();
       }
     }
   } else if (warp == 1) {
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
         }
       }
       if (S > 1) {
-        cluster_sync_all();
-        cluster_sync_all();
+        mm_cluster_sync();
+        mm_cluster_sync();
       }
     }
     if (elect_one()) mma_commit(drain);
@@ -342,14 +345,14 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
 #pragma unroll
         for (int i = 0; i < NN; ++i)
           if (i < rows) part[i * NM + col] = acc[i];
-        cluster_sync_all();
+        mm_cluster_sync();
         const uint32_t mine = smem_u32(part) + (uint32_t)col * 4;
         for (int i = rank; i < rows; i += S) {
           float sum = 0.f;
           for (int j = 0; j < S; ++j) sum += peer_f32(mine + (uint32_t)i * (NM * 4), (uint32_t)j);
           if (in && ok) dst[(size_t)i * args.m] = __float2bfloat16_rn(sum);
         }
-        cluster_sync_all();  // everyone has read this CTA's partial tile
+        mm_cluster_sync();  // everyone has read this CTA's partial tile
       }
     }
   }

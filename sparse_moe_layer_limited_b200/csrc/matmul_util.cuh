@@ -105,6 +105,13 @@ __device__ __forceinline__ bool mm_wait_thread(uint64_t* bar, uint32_t parity, u
   }
 }
 
+// The aligned cluster barrier wants the warp's lanes together; code that lets them
+// go different ways (stores of a tile's edge, one lane's arrive) comes before it.
+__device__ __forceinline__ void mm_cluster_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
 // Arrive on a barrier of the pair's other CTA (shared::cluster address) without
 // a cluster-scope release: for hand-overs that order no memory, only TMEM reads
 // (which tcgen05.fence orders around the barrier).  With release and acquire at
