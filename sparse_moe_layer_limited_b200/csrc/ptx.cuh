@@ -73,9 +73,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the status word tells a wait to give up: a wait that ran out, or counts
+// that contradict the indices.  A bad index does not: the call that met it, on
+// whatever workspace, has skipped it, and later calls on that workspace are good.
+__device__ __forceinline__ bool wait_is_lost(const uint32_t* err) {
+  return (*reinterpret_cast<const volatile uint32_t*>(err) & ~kErrBadIndex) != 0u;
+}
+
 // Wait for the phase with the given parity to complete.  Gives up after
-// `limit_ns` of wall time, or as soon as another CTA has flagged an error in
-// `*err`; on giving up it ORs kErrWaitTimeout into *err and returns false.
+// `limit_ns` of wall time, or as soon as wait_is_lost; when the time has run
+// out it ORs kErrWaitTimeout into *err.  Returns false on giving up.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
                                                   uint32_t* err, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -83,7 +90,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 0) {
-      if (*reinterpret_cast<volatile uint32_t*>(err) != 0u) return false;
+      if (wait_is_lost(err)) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
         atomicOr(err, kErrWaitTimeout);
         return false;
@@ -112,7 +119,7 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 255u) == 0) {
-      if (*reinterpret_cast<volatile uint32_t*>(err) != 0u) return false;
+      if (wait_is_lost(err)) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
         atomicOr(err, kErrWaitTimeout);
         return false;

@@ -209,3 +209,24 @@ def test_calls_on_several_streams_at_once(M):
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
     assert M.moe_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [1, 3], ids=["bf16", "e4m3"])
+def test_bad_offsets_on_a_layers_workspace_do_not_disturb_the_layer(M, dtype):
+    """Any workspace serves the products.  Bad offsets leave their bit in the layer's status word;
+    the layer's own kernels, whose waits are long here, still finish."""
+    cfg = CONFIGS[dtype].with_(T=2048, d=1024, N=16, K=4, G=4, topG=2, f=512)
+    s = S.moe_shape(cfg)
+    Rw, b = torch.from_numpy(gen.make_router(cfg)).cuda(), torch.from_numpy(gen.make_bias(cfg)).cuda()
+    W = S.device_weights(cfg)
+    x = S.to_dev_x(gen.make_x(cfg, 0, 0), cfg)
+    layer = M.MoELayer(s, Rw, b, W["w13"], W["w2"], W.get("w13_scales"), W.get("w2_scales"), gamma=0.0)
+    want = layer.forward(x).clone()
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rows, w = (torch.randn(*sh, generator=g, device="cuda").to(BF) for sh in ((40, 64), (3, 32, 64)))
+    off = torch.tensor([0, 10, 5, 40], dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        M.moe_grouped_matmul(rows, off, w, torch.empty(40, 32, dtype=BF, device="cuda"), layer.ws)
+        layer.y.zero_()
+        assert torch.equal(layer.forward(x), want)
+        assert layer.device_status() == 4      # MOE_DEV_BAD_INDEX, and nothing else
