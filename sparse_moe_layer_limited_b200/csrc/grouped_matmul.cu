@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       for (int u = pair; u < total && ok; u += npairs) {
         const Unit t = decode(u);
         for (int j = 0; j < t.tiles && ok; ++j, ++use) {
-          ok = mm_wait_thread(&edone[use & 1], (use >> 1) & 1, args.status);
+          ok = mm_wait_thread(&edone[use & 1], (use >> 1) & 1, args.status, contraction_ms(t.kb));
           if (ok) mbar_arrive_peer(tempty0 + 8u * (uint32_t)(use & 1));
         }
       }
@@ -446,15 +446,19 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
   } else if (kMode == kDw && warp == 2 + kEpiWarps) {
     // ---- rows past an expert's end, in its last 16-row step: one 128-byte line
     // per row and 64-wide chunk ----
-    int kbs = 0;  // K blocks of the units so far
+    int kbs = 0;    // K blocks of the units so far
+    int since = 0;  // of those after the last wait
     uint32_t tphase = 0;
     const uint32_t tclear0 = mapa_shared(smem_u32(&tclear[0]), 0);
     for (int u = pair; u < total; u += npairs) {
       const Unit t = decode(u);
       kbs += t.kb;
+      since += t.kb;
       if (!ragged_end(t)) continue;
       const int stage = (kbs - 1) % kStages;
-      if (!mm_wait(&tland[stage], (tphase >> stage) & 1u, args.status)) break;
+      if (!mm_wait(&tland[stage], (tphase >> stage) & 1u, args.status, contraction_ms(since)))
+        break;
+      since = 0;
       tphase ^= 1u << stage;
       uint8_t* sm = base + (size_t)stage * kStageBytes;
       const int valid = t.rows - (t.kb - 1) * GBK, lines = ((valid + 15) & ~15) - valid;
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(pair_threads(kMode), 1) grouped_matmul_pair_ke
       const int m = t.m0 + (int)rank * kHalf + q * 32;  // this warp's first M index
       for (int j = 0; j < t.tiles; ++j, ++use) {
         const int acc = use & 1;
-        ok = mm_wait(&tfull[acc], (use >> 1) & 1, args.status);
+        ok = mm_wait(&tfull[acc], (use >> 1) & 1, args.status, contraction_ms(t.kb));
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * GN;

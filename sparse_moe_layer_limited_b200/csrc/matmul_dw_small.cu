@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(DThreads, 1) matmul_dw_small_kernel(
       const Unit t = decode(u);
       const uint32_t buf = use & 1u;
       if (t.kcnt > 0 && ok) {
-        ok = mm_wait(&tfull[buf], (use >> 1) & 1u, args.status);
+        ok = mm_wait(&tfull[buf], (use >> 1) & 1u, args.status, contraction_ms(t.kcnt));
         ++use;
       }
       if (ok) {

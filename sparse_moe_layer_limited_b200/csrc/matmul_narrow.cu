@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(NThreads, 1) matmul_narrow_kernel(
         }
       } else if (kcnt > 0 && ok) {
         const uint32_t buf = use % NBufs;
-        ok = mm_wait(&tfull[buf], (use / NBufs) & 1u, args.status);
+        ok = mm_wait(&tfull[buf], (use / NBufs) & 1u, args.status, contraction_ms(kcnt));
         if (ok) {
           tc_fence_after();
           uint32_t p[32];

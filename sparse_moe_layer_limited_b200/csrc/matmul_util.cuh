@@ -11,6 +11,11 @@ namespace moe {
 constexpr int kMatmulMaxGroups = 384;  // tile table entries that fit beside the operand ring
 // Waits are timed in steps of 2^20 ns (about a millisecond), in 32 bits.
 constexpr uint32_t kMatmulTimeoutMs = 2000, kDrainMs = 50;
+// A wait for a whole contraction of `blocks` K blocks: 2 us a block beside that
+// (they take 0.1 to 0.6), as an expert may own 2^31 rows and these are its blocks.
+__device__ __forceinline__ uint32_t contraction_ms(int blocks) {
+  return kMatmulTimeoutMs + (uint32_t)blocks / 500u;
+}
 __device__ __forceinline__ uint32_t clock_ms() { return (uint32_t)(globaltimer_ns() >> 20); }
 
 // One try of a wait.  `cluster`: cluster-scope acquire, for barriers that the

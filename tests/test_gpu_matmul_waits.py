@@ -75,3 +75,29 @@ def test_a_recorded_time_out(M, op, counts, n, k):
         call(ws)
         torch.cuda.synchronize()
         assert M.moe_read_device_status(ws) == 0 and torch.equal(out, want)
+
+
+def test_a_contraction_that_takes_longer_than_the_limit(M):
+    """One of 80 experts owns 700 million rows: one pair of CTAs adds them, for some 2.7 s, and the
+    warps that wait for it must not give up after 2.  All but 400 rows are zeros, so the sum has 400
+    terms: at most 400 steps of 2^-23 of the terms' magnitudes, and one rounding to bf16."""
+    R, E, c = 700_000_005, 80, 8
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    dy, x = (torch.zeros(R, c, dtype=BF, device="cuda") for _ in range(2))
+    at = torch.cat([torch.arange(0, R, R // 390 + 1, device="cuda"),
+                    torch.arange(R - 17, R, device="cuda")])[-400:]
+    dy[at], x[at] = rand(6, len(at), c), rand(7, len(at), c)
+    off = torch.full((E + 1,), R, dtype=torch.int32, device="cuda")
+    off[0] = 0
+    dw = torch.full((E, c, c), 7.0, dtype=BF, device="cuda")
+    ws = torch.zeros(M.matmul_workspace_size(), dtype=torch.uint8, device="cuda")
+    M.moe_grouped_matmul_dw(dy, x, off, dw, ws)
+    assert M.moe_read_device_status(ws) == 0
+    a, b = dy[at].double(), x[at].double()
+    want, mag = a.t() @ b, a.abs().t() @ b.abs()
+    err = mag * 400 * 2.0 ** -23
+    err = err + (want.abs() + err) * 2.0 ** -8
+    assert ((dw[0].double() - want).abs() <= err).all() and (dw[1:] == 0).all()
+    del dy, x
+    torch.cuda.empty_cache()
