@@ -73,11 +73,25 @@ class MoELayer:
         """The layer's rows after the norm in front of it (x itself without one)."""
         if self.norm_w is None:
             return x
+        self._before_norm(x)
         L.moe_layer_norm(x, self.norm_w, self.norm_b, self.norm_eps, self.x_norm, self.norm_mean,
                          self.norm_rstd, stream)
         return self.x_norm
 
+    def _before_norm(self, x):
+        """Refuse the rows after the norm where those before it are read."""
+        if self.norm_w is not None and x.data_ptr() == self.x_norm.data_ptr():
+            raise ValueError("x: the rows before the norm in front of the layer are read here, "
+                             "these are the ones that norm(x) returned")
+
+    def _normed(self, x):
+        """Refuse rows before the norm where those after it are read."""
+        if self.norm_w is not None and x.data_ptr() != self.x_norm.data_ptr():
+            raise ValueError("x: with a norm in front of the layer, the experts take the rows that "
+                             "norm(x) returned")
+
     def route(self, x, stream=None):
+        """Router on the rows before the norm (norm(x) runs here)."""
         s = self.shape
         x = self.norm(x, stream)
         L.moe_route(s, x, self.router_w, self.bias, self.topk_idx, self.topk_gate, self.counts,
@@ -99,7 +113,9 @@ class MoELayer:
 
     def experts_and_combine(self, x, stream=None):
         """The expert GEMMs and the COMBINE step (one fused launch pair when
-        fused_combine is set) on the rows after the norm; writes self.y."""
+        fused_combine is set); writes self.y.  With a norm in front, x is what
+        norm(x) returned; other rows are refused."""
+        self._normed(x)
         s = self.shape
         if self.fused_combine:
             L.moe_expert_ffn_combine(s, self.x_perm, self.offsets, self.perm_tok, self.slot,
@@ -111,7 +127,9 @@ class MoELayer:
                           stream)
 
     def experts(self, x, stream=None):
-        """The expert GEMMs on the dispatched rows (gathered from x or read from x_perm)."""
+        """The expert GEMMs on the dispatched rows (gathered from x or read from x_perm); x as at
+        experts_and_combine."""
+        self._normed(x)
         s = self.shape
         if self.gather:
             L.moe_expert_ffn_gathered(s, x, self.perm_tok, self.offsets, self.w13, self.w2,
@@ -136,6 +154,7 @@ class MoELayer:
         s = self.shape
         if s.dtype != L.DTYPE_BF16 or self.gather:
             raise ValueError("the layer backward runs in BF16 mode on the x_perm path")
+        self._before_norm(x)
         dev, xdt = x.device, L.x_torch_dtype(s)
         if getattr(self, "_bwd", None) is None:
             self._bwd = dict(
