@@ -47,9 +47,11 @@
 // shared memory (in both operands, as 0 * NaN is NaN) before the MMA reads them.
 //
 // Roles per CTA: warp 0 TMA producer; warp 1 TMEM owner, in the pair's leader
-// MMA issuer, in its peer forwarding accumulator releases; warps 2-9 drain one
-// accumulator (fp32, rounded once to bf16) while the next tile accumulates in
-// the other; warp 10 (weight gradient) clears the rows past an expert's end.
+// MMA issuer, in its peer forwarding accumulator releases; warps 2-9 drain the
+// accumulators (fp32, rounded once to bf16): with one tile a unit one of them,
+// while the next tile accumulates in the other; with two tiles a unit both, and
+// the next unit's products wait for that.  Warp 10 (weight gradient) clears the
+// rows past an expert's end.
 // Waits are bounded and set the status word when they give up.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -317,7 +317,7 @@ cudaError_t launch(SArgs a, long long units, int kdim, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const long long most = 148 * 32 / a.splits;
+  const long long most = num_sms() * 32 / a.splits;
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * a.splits), 1, 1);
   return note_cuda(cudaLaunchKernelEx(&cfg, kernel, a), "fp32 grouped matmul launch");
 }

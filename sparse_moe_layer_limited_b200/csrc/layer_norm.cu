@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT,
   if (r < R) cur.load(x + (size_t)r * d, t, d);
   // with several warps a row, every warp of the CTA sees the same r
   for (int it = 0; r < R; r += step, ++it) {
-    if (r + step < R && r + step > r) next.load(x + (size_t)(r + step) * d, t, d);
+    if (r + step < R) next.load(x + (size_t)(r + step) * d, t, d);
     Stat s{0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
@@ -168,11 +168,10 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT,
       if (c < d) *reinterpret_cast<typename RowRegs<T, VEC, PIECES, kT>::Piece*>(yrow + c) = o;
     }
     cur = next;
-    if (r + step < r) break;  // the row index would pass 2^31
   }
 }
 
-// ---- rows of 16-byte pieces, one thread per piece -------------------------------------
+// ---- rows of 16-byte pieces, two or four to a thread -------------------------------------
 __device__ __forceinline__ float both(f32x2 v) {
   const float2 f = split2(v);
   return f.x + f.y;
@@ -674,7 +673,7 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT,
   const float inv_d = 1.f / (float)d;
   for (int it = 0; r < R; r += step, ++it) {
     const float mu = mean[r], rs = rstd[r];
-    if (r + step < R && r + step > r) {
+    if (r + step < R) {
       nx.load(x + (size_t)(r + step) * d, t, d);
       nd.load(dy + (size_t)(r + step) * d, t, d);
     }
@@ -732,7 +731,6 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT,
     }
     cx = nx;
     cd = nd;
-    if (r + step < r) break;
   }
   float* prow = part + (size_t)blockIdx.x * 2 * d;
   if constexpr (kGroups > 1) {
@@ -832,10 +830,10 @@ int bwd_ctas(int R, int d, int elem) {
   const bool rows = by_rows(d, elem);
   const int groups = !rows && d <= 512 ? 4 : 1;
   const long long want = ((long long)R + groups - 1) / groups;
-  const long long most = 148LL * (rows         ? rows_per_sm(d, elem, bwd_pieces(d, elem))
-                                  : d <= 2048 ? 4
-                                  : d <= 4096 ? 2
-                                              : 1);  // 512 threads or more
+  const long long most = num_sms() * (rows        ? rows_per_sm(d, elem, bwd_pieces(d, elem))
+                                      : d <= 2048 ? 4
+                                      : d <= 4096 ? 2
+                                                  : 1);  // 512 threads or more
   return (int)(want < most ? (want < 1 ? 1 : want) : most);
 }
 
@@ -859,7 +857,7 @@ template <typename T, int VEC, int PIECES, int kT>
 void go(const Fwd& a, cudaStream_t st) {
   constexpr int kBlock = kT < 128 ? 128 : kT;
   const long long want = ((long long)a.R + kBlock / kT - 1) / (kBlock / kT);
-  const int cap = 148 * (1024 / kBlock);
+  const int cap = num_sms() * (1024 / kBlock);
   layer_norm_kernel<T, VEC, PIECES, kT><<<(int)(want < cap ? want : cap), kBlock, 0, st>>>(
       static_cast<const T*>(a.x), a.w, a.b, a.eps, a.R, a.d, static_cast<T*>(a.y), a.mean, a.rstd);
 }
@@ -881,7 +879,7 @@ cudaError_t rows_launch(const Fwd& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        most_smem);
   if (e != cudaSuccess) return e;
-  const int most = 148 * rows_per_sm(a.d, sizeof(T), PIECES);
+  const int most = num_sms() * rows_per_sm(a.d, sizeof(T), PIECES);
   kernel<<<a.R < most ? a.R : most, kT, S * PIECES * kT * 16, st>>>(
       static_cast<const T*>(a.x), a.w, a.b, a.eps, a.R, a.d, static_cast<T*>(a.y), a.mean, a.rstd);
   return cudaGetLastError();

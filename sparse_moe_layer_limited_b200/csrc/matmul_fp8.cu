@@ -612,7 +612,8 @@ cudaError_t launch_quantize_rows_fp8(const void* x, long long rows, int cols, in
                                      cudaStream_t st) {
   const long long tiles = rows * ((cols + QB - 1) / QB);
   long long blocks = (tiles * 16 + 255) / 256;
-  if (blocks > 148 * kQuantCtas) blocks = 148 * kQuantCtas;
+  const long long most = num_sms() * kQuantCtas;
+  if (blocks > most) blocks = most;
   auto kernel = e5m2 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>;
   kernel<<<(int)blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, codes,
                                       scales, sc_ld);
