@@ -86,9 +86,9 @@ enum {
 
 /* Device status bits (moe_read_device_status). */
 enum {
-  MOE_DEV_WAIT_TIMEOUT = 1,   /* a tensor-core pipeline wait gave up after ~2 s */
+  MOE_DEV_WAIT_TIMEOUT = 1,   /* a tensor-core pipeline wait gave up (~2 s) */
   MOE_DEV_COUNT_MISMATCH = 2, /* counts[] disagree with the expert indices */
-  MOE_DEV_BAD_INDEX = 4       /* an expert index outside [0, N) */
+  MOE_DEV_BAD_INDEX = 4       /* an expert index outside [0, N), or refused offsets */
 };
 
 /* Human-readable text for a MOE_* status.  Never NULL; static storage. */
@@ -474,7 +474,10 @@ int moe_forward(const moe_shape* shape, const void* x, const float* router_w, fl
  * `ws`: moe_matmul_workspace_size() bytes, 256-byte aligned, zeroed once
  * (moe_workspace_init); it holds the status word, so any workspace of this
  * library serves, and calls on several streams or captured graphs may share
- * it.  After MOE_DEV_WAIT_TIMEOUT clear it before the next call.
+ * it.  MOE_DEV_BAD_INDEX on record disturbs no later call, here or in the
+ * layer.  Waits give up after about 2 s, those for a whole BF16 contraction
+ * after 2 us more for each 64 of its indexes; after MOE_DEV_WAIT_TIMEOUT the
+ * call's results are lost: clear the word before the next call.
  *
  * Supported: experts <= 384; for BF16 n and k multiples of 8; for FP8 k (and
  * for the input gradient n) a multiple of 16; rows and widths below 2^31 - 65536

@@ -27,17 +27,18 @@
 // an expert share one unit: each W block is staged once for both, and both
 // accumulators (256 TMEM columns each) are filled.  Where the last round would
 // leave most pairs idle its experts' units are cut in two again (ragged_schedule;
-// forward of 32 x 512 rows, 2048 x 4096: 343 -> 322 us, of 64 x about 400 rows,
-// 1536 x 2048: 197 -> 183).
+// called back to back, forward of 32 x 512 rows, 2048 x 4096: 245 us, uncut 249;
+// of 64 x about 400 rows, 1536 x 2048: 179 and 183).
 //
-// Measured, bf16: 8192 x 4096 x 7168 dense forward 318 us in a burst (1.51
-// PFLOP/s), 369 us under sustained power, level with the library's product of
-// that shape; 65536 rows of 256 experts, 2048 x 7168: 1.64 ms in a burst, 2.2
-// sustained; weight gradients of 32 experts, 16384 skewed rows, 4096 x 7168: 0.90
-// and 1.11 ms, bound by stores where experts are small (a pure fill of memory
-// runs at 3.9 TB/s).  The loops of the issuing warps are walked by the whole warp
-// with one elected lane issuing: from one lane of a diverged branch the same
-// kernel was 12-18% slower.
+// Measured, bf16, in a burst and after a second of it (the 1000 W cap): 8192 x
+// 4096 x 7168 dense forward 311 us (1.55 PFLOP/s) and 367, level with the
+// library's product of that shape; 65536 rows of 256 experts, 2048 x 7168: 1.70
+// and 2.0 to 2.25 ms; input gradient of 24576 rows of 64 experts, 1408 x 2048: 127
+// and 155 us; weight gradients of 32 experts, 16384 skewed rows, 4096 x 7168: 1.01
+// and 1.11 ms, bound by stores where experts are small (a pure fill of memory runs
+// at 3.9 TB/s).  The loops of the issuing warps are walked by the whole warp with
+// one elected lane issuing: from one lane of a diverged branch the same kernel was
+// 12-18% slower.
 //
 // Units are ordered expert-major, then in blocks of N tiles (raster below): pairs
 // running side by side share weights and rows through L2, and each expert's weights stream
@@ -115,9 +116,11 @@ __device__ __forceinline__ int row_tile(int rows, int tiles) {
 // Tile (m, n) of an expert's unit `local`: blocks of kBlockN N tiles, within a
 // block M tile by M tile.  The pairs at work then share kBlockN tiles of the N
 // operand and as many of the M operand as there are pairs to a block row, in
-// place of the whole N operand.  (8192 x 4096 x 7168 forward under sustained
-// power: 398 us without blocks, 377 with 4, 369 with 8 to 16; weight gradients
-// of 32 experts with 16384 skewed rows: 985 us in a burst without, 905 with 12.)
+// place of the whole N operand.  (us with no blocks, blocks of 4, 8, 12, 16:
+// forward 8192 x 4096 x 7168 385, 367, 361, 365, 362; 16384 x 2048 x 2048 112, 106,
+// 107, 108, 108; weight gradients of 8192 rows, 7168 x 7168 694, 669, 650, 656, 652,
+// of 32 experts with 16384 skewed rows, 4096 x 7168 1164, 1144, 1135, 1137, 1138.
+// Four more shapes differ by less than 3% between blocks of 8 to 16.)
 constexpr int kBlockN = 12;
 __device__ __forceinline__ void raster(int local, int MT, int NT, int& m, int& n) {
   const int b = local / (MT * kBlockN), rest = local - b * (MT * kBlockN);

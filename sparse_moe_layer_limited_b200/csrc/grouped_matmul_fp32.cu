@@ -4,18 +4,19 @@
 //
 // A CTA of 256 threads owns a BM x BN output tile; each thread keeps TM x TN
 // running sums in registers and adds one contraction index at a time, so a
-// sum is a plain fp32 chain (two columns to a packed multiply-add).  Slices of 16 contraction indexes go through two
-// shared-memory buffers in turn; the next slice's loads are issued before the
-// current one is multiplied.  Tiles by size: 128 x 128 (two CTAs an SM) where
-// they fill the SMs, 64 x 64 below that, 16 x 128 for experts of few rows.
-// Small problems split the contraction over a cluster of up to 8 CTAs, whose
-// partial tiles are added rank by rank, in order, through distributed shared
-// memory.
+// sum is a plain fp32 chain (two columns to a packed multiply-add).  Slices of 16
+// contraction indexes go through two shared-memory buffers in turn; the next
+// slice's loads are issued before the current one is multiplied.  Tiles by size:
+// 128 x 128 (two CTAs an SM) where they fill the SMs, 64 x 64 below that, 16 x 128
+// for experts of few rows.  Small problems split the contraction over a cluster of
+// up to 8 CTAs, whose partial tiles are added rank by rank, in order, through
+// distributed shared memory.
 //
-// Measured: 8 experts x 1024 rows, 1024 x 1024: 399 us (43 TFLOP/s; the fp32
-// library product by expert 377), 64 rows of 2000 x 2000 25 us (37), 16 rows of
-// two 4096 x 4096 68 us (181).  8 x 8 sums a thread issue 4 shared loads and 32
-// packed multiply-adds per contraction index; the multiply-add pipe bounds it.
+// Measured (in brackets without splits and the smaller tile): 8 experts x 1024
+// rows, 1024 x 1024: 396 us (43 TFLOP/s; the fp32 library product by expert takes
+// 377), 64 rows of 2000 x 2000 25 us (37), 16 rows of two 4096 x 4096 78 us (181).
+// 8 x 8 sums a thread issue 4 shared loads and 32 packed multiply-adds per
+// contraction index; the multiply-add pipe bounds it.
 #include <cuda_runtime.h>
 
 #include "internal.h"

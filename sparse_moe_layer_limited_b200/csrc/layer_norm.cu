@@ -645,7 +645,9 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) row_bwd_kernel(
 // One partial row of dw and db per CTA: part [gridDim.x][2][d].  Absent pieces
 // are zeros (times the first weight) and need no branch, and a thread has 16
 // elements at most: 8192 x 7001 bf16 129 us (215 with branches and 32 elements,
-// 256 threads a row), 4000 x 15001 382 us (1200).
+// 256 threads a row), 4000 x 15001 382 us (1200).  The 1024-thread forms, above
+// 8192 columns, spill some 650 bytes a thread: fp32 4000 x 16384 384 us (the
+// forward, 512 threads, 98).
 template <typename T, int VEC, int PIECES, int kT>
 __global__ void __launch_bounds__(kT < 128 ? 128 : kT,
                                  kT < 128 ? 4 : kT < 512 ? 512 / kT : 1) layer_norm_bwd_kernel(

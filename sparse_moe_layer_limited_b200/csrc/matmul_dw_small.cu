@@ -7,8 +7,8 @@
 // the cluster adds them, rank by rank, in order (every CTA takes its share of the
 // tile), through distributed shared memory.  No workspace, no atomics.
 //
-// Measured (in brackets the pair kernel): 24415 rows of 3296 x 40 42 us (105),
-// 16384 of 1024 x 1024 44 us (79), 100000 of 64 x 64 50 us (248): bound by what an
+// Measured (in brackets the pair kernel): 24415 rows of 3296 x 40 43 us (105),
+// 16384 of 1024 x 1024 45 us (79), 100000 of 64 x 64 50 us (248): bound by what an
 // SM pulls, 32 KB of operands for 256 cycles of MMA, and by how many take part.
 // Not split, on 75 to 148 units, it is level with the pair kernel (16384 rows of
 // 256 x 7168 85 us against 81), which therefore keeps those calls.

@@ -12,15 +12,15 @@
 // a thread, while the next slice fills the other buffer.  The scales are read
 // from global memory two slices ahead.  The result is rounded once to bf16.
 //
-// 8192 x 4096 x 7168: 245 us at 1.8 GHz (1.96 PFLOP/s), 293 us under sustained
-// power; 16411 skewed rows of 64 experts, input gradient, 2048 x 7168: 380 and
-// 445 us.  Of a slice's 1100 cycles 512 are MMA; without the promotion's reads
-// of TMEM the first takes 197 us, with half the operand traffic as well 170 us,
-// without the multiply-adds no less than with them.  The next unit and its
-// first scales are looked up before a unit is stored, in 32-column pieces
-// through two buffers (before that the second case took 398 us).  Measured and
-// not taken: CTA pairs (a third less operand traffic: 240 us dense, but 256-row
-// tiles cost ragged experts 25%).
+// 8192 x 4096 x 7168: 238 us in a burst (2.02 PFLOP/s), 280 us under sustained
+// power; 16411 skewed rows of 64 experts, 2048 x 7168: input gradient 365 and 427
+// to 440 us, forward 336 and 398.  Of a slice's 1100 cycles 512 are MMA; without
+// the promotion's reads of TMEM the first took 197 us (when the kernel took 245),
+// with half the operand traffic as well 170 us, without the multiply-adds no less
+// than with them.  The next unit and its first scales are looked up before a unit
+// is stored, in 32-column pieces through two buffers.  Measured and not taken: CTA
+// pairs (a third less operand traffic: 240 us dense, but 256-row tiles cost ragged
+// experts 25%).
 //
 // Also here: the quantisers that make the codes, per 1x128 tile of a row and
 // per 128x128 block (tile_scale below).
@@ -510,6 +510,8 @@ __global__ void __launch_bounds__(256, kQuantCtas) quantize_rows_kernel(
 
 // One 128x128 block of one matrix per CTA of 128 threads: sixteen lanes cover a
 // row's 128 columns with 16-byte loads, kept in registers for the second pass.
+// 32 x 2048 x 7168: 225 us (6.3 TB/s of the 3 bytes a weight that it cannot do
+// without), one 4096 x 7168 14.4 us.
 __global__ void __launch_bounds__(128) quantize_blocks_kernel(const __nv_bfloat16* __restrict__ w,
                                                               int n, int k, int nb, int kb,
                                                               uint8_t* __restrict__ q,

@@ -11,9 +11,9 @@
 // order (every CTA takes its share of the rows), through distributed shared
 // memory.  No workspace, no atomics.
 //
-// Measured: one row of 2048 x 7168 bf16 17 us (27 on the pair kernel), 8 rows on
-// 8 experts of 2048 x 7168 45 us (5.3 TB/s of weights), FP8 7 rows of 7168 x 2048
-// 9.6 us (14.8), 64 rows of 4096 x 7168 17 us (31); 6-7 us of each are start and
+// Measured: one row of 2048 x 7168 bf16 16.4 us (27 on the pair kernel), 8 rows on
+// 8 experts of 2048 x 7168 45 us (5.2 TB/s of weights), FP8 7 rows of 7168 x 2048
+// 9.7 us (14.8), 64 rows of 4096 x 7168 16.4 us (31); 6-7 us of each are start and
 // end (tensor memory, barriers, first copies, the cluster's two barriers).
 //
 // FP8: every 128-wide slice is one product into its own TMEM buffer (eight of
@@ -398,7 +398,14 @@ long long narrow_units(int R, int E, int cols) {
 }  // namespace
 
 // The narrow kernel takes a call whose units all fit on the SMs at once (so
-// none waits for a second round, which the pair kernels overlap better).
+// none waits for a second round, which the kernels for many rows overlap better).
+// us here and there, 2048 x 7168, called back to back:
+//   units                                  32       64       128      144      160
+//   bf16 forward, one expert             21 / 35  30 / 41  35 / 41  35 / 33  63 / 37
+//   bf16 forward, a row for each expert     -     25 / 31  45 / 45  49 / 49  75 / 71
+//   FP8 forward, one expert              18 / 49  27 / 34  31 / 33  31 / 33  54 / 33
+//   FP8 forward, a row for each expert      -     16 / 32  33 / 34  33 / 35  50 / 35
+// The input gradients run as the forwards do.
 bool matmul_is_narrow(int R, int E, int cols) { return narrow_units(R, E, cols) <= num_sms(); }
 
 // Argument meanings as at launch_grouped_matmul_bf16 and launch_matmul_fp8;

@@ -189,6 +189,7 @@ class MoELayer:
             if "norm" not in B:
                 B["norm"] = torch.empty(L.layer_norm_workspace_size(s.T, s.d), dtype=torch.uint8,
                                         device=dev)
+            # dx has been rounded to the layer's type once, as it leaves a layer without a norm
             out["dx"] = torch.empty_like(dx)
             out["dnorm_w"] = torch.empty_like(self.norm_w)
             if self.norm_b is not None:
